@@ -134,6 +134,17 @@ def lib():
             "bitopt_step_multi_planned": ([ctypes.POINTER(MultiPlanC), HP, i32, P, P, P], ctypes.c_int),
             "bitopt_device_scalars_bytes": ([], i64),
             "bitopt_device_scalars_write": ([HP, i32, P, i64], ctypes.c_int),
+            "bitopt_mx_code_bytes": ([i64, i32], i64),
+            "bitopt_mx_scale_bytes": ([i64], i64),
+            "bitopt_mx_quantize": ([P, i32, i64, i64, i64, i32, P, P, P], ctypes.c_int),
+            "bitopt_mx_dequantize": ([P, P, i32, i64, i64, P, i32, i64, P], ctypes.c_int),
+            "bitopt_mx_matmul": ([P, P, i32, P, P, i32, i64, i64, i64, P, i32, i64, P], ctypes.c_int),
+            "bitopt_mx_linear": ([P, i32, i64, P, P, i32, i64, i64, i64, P, i32, i64, P], ctypes.c_int),
+            "bitopt_mx_linear_grad_input": ([P, i32, i64, P, P, i32, i64, i64, i64, P, i32, i64, P], ctypes.c_int),
+            "bitopt_mx_linear_grad_weight": ([P, i32, i64, P, P, i32, i64, i64, i64, P, i32, i64, i32, P],
+                                             ctypes.c_int),
+            "bitopt_swiglu_forward_mx8": ([P, P, i32, i64, i64, i64, i64, P, i64, P, P, P, P, P], ctypes.c_int),
+            "bitopt_swiglu_backward_mx8": ([P, i32, i64, i64, i64, P, P, P, P, P, i64, P, i64, P], ctypes.c_int),
             "bitopt_step_multi_planned_dscalars": ([ctypes.POINTER(MultiPlanC), HP, P, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
@@ -545,3 +556,214 @@ def step_multi(hp, step, tensors, qmap1=None, qmap2=None, workspace=None, stream
     _check(lib().bitopt_step_multi(ctypes.byref(h), int(step), arr, len(tensors), _ptr(qmap1), _ptr(qmap2),
                                    _ptr(workspace), workspace.numel(), _stream(stream)))
     return workspace
+
+
+# ------------------------------------------------------------------- MX matrices
+
+MX_FORMATS = {"e2m1": 0, "e4m3": 1}
+
+
+def mx_code_bytes(cols: int, fmt: str = "e2m1") -> int:
+    """Bytes of codes in one row of an MX matrix: rows are padded to 128 elements."""
+    return (cols + 127) // 128 * (64 if _mx_format(fmt) == 0 else 128)
+
+
+def mx_scale_bytes(cols: int) -> int:
+    """Scale bytes in one row of an MX matrix."""
+    return (cols + 127) // 128 * 4
+
+
+def _mx_format(fmt):
+    f = MX_FORMATS.get(fmt)
+    if f is None:
+        raise ValueError(f"unknown MX format {fmt!r} (one of {sorted(MX_FORMATS)})")
+    return f
+
+
+def _rows(t, name, device=None):
+    """A device matrix with contiguous rows: (distance of its rows in elements)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    s = t.stride()
+    if s[1] != 1 and t.size(1) > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous (strides {s})")
+    if t.size(0) > 1 and s[0] < t.size(1):
+        raise ValueError(f"{name}: its rows overlap (strides {s})")
+    return s[0] if t.size(0) > 1 else t.size(1)
+
+
+def _mx_operand(codes, scales, cols, fmt, name, device):
+    """Checks an MX matrix of `cols` columns; returns its rows."""
+    f = _mx_format(fmt)
+    for t, what, width in ((codes, "codes", mx_code_bytes(cols, fmt)), (scales, "scales", mx_scale_bytes(cols))):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name} {what}: expected torch.uint8, got {t.dtype}")
+        if t.dim() != 2 or t.size(1) != width or not t.is_contiguous():
+            raise ValueError(f"{name} {what}: expected a contiguous matrix of {width} bytes a row for {cols} {fmt} "
+                             f"columns, got shape {tuple(t.shape)}")
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{name} {what} must be on {device}")
+        if t.size(0) != codes.size(0):
+            raise ValueError(f"{name}: {codes.size(0)} rows of codes but {t.size(0)} of scales")
+    return f, codes.size(0)
+
+
+class _On:
+    """Makes `device` current, and `stream` the stream of the results allocated inside:
+    memory a caller's stream writes then belongs to that stream."""
+
+    def __init__(self, device, stream):
+        self._guards = []
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the arguments on {device}")
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _mx_result(out, shape, dtype, device, name):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out, _rows(out, name, device)
+
+
+def _mx_new(codes, scales, rows, cols, fmt, device, name):
+    if codes is None:
+        codes = torch.empty((rows, mx_code_bytes(cols, fmt)), dtype=torch.uint8, device=device)
+    if scales is None:
+        scales = torch.empty((rows, mx_scale_bytes(cols)), dtype=torch.uint8, device=device)
+    f, n = _mx_operand(codes, scales, cols, fmt, name, device)
+    if n != rows:
+        raise ValueError(f"{name}: expected {rows} rows of codes, got {n}")
+    return codes, scales, f
+
+
+def mx_quantize(x, fmt: str = "e2m1", codes=None, scales=None, stream=None):
+    """The MX form of a matrix: (codes, scales), blocks of 32 along its rows."""
+    ldx, dt = _rows(x, "x"), _dt(x)
+    rows, cols = x.shape
+    with _On(x.device, stream) as s:
+        codes, scales, f = _mx_new(codes, scales, rows, cols, fmt, x.device, "the result")
+        _check(lib().bitopt_mx_quantize(x.data_ptr(), dt, rows, cols, ldx, f, codes.data_ptr(), scales.data_ptr(), s))
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, cols: int, fmt: str = "e2m1", out=None, dtype=torch.float32, stream=None):
+    """The values of an MX matrix of `cols` columns."""
+    f, rows = _mx_operand(codes, scales, cols, fmt, "the input", codes.device)
+    with _On(codes.device, stream) as s:
+        out, ldo = _mx_result(out, (rows, cols), dtype, codes.device, "out")
+        _check(lib().bitopt_mx_dequantize(codes.data_ptr(), scales.data_ptr(), f, rows, cols, out.data_ptr(), _dt(out),
+                                          ldo, s))
+    return out
+
+
+def mx_matmul(a_codes, a_scales, b_codes, b_scales, k: int, a_fmt: str = "e2m1", b_fmt: str = "e2m1", out=None,
+              dtype=torch.bfloat16, stream=None):
+    """a b^T for MX matrices a (m x k) and b (n x k)."""
+    fa, m = _mx_operand(a_codes, a_scales, k, a_fmt, "a", a_codes.device)
+    fb, n = _mx_operand(b_codes, b_scales, k, b_fmt, "b", a_codes.device)
+    with _On(a_codes.device, stream) as s:
+        out, ldo = _mx_result(out, (m, n), dtype, a_codes.device, "out")
+        _check(lib().bitopt_mx_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(),
+                                      b_scales.data_ptr(), fb, m, n, k, out.data_ptr(), _dt(out), ldo, s))
+    return out
+
+
+def mx_linear(x, w_codes, w_scales, fmt: str = "e2m1", out=None, dtype=None, stream=None):
+    """x W^T for a 16-bit x (tokens x k) and MX weights W (n x k); dtype defaults to x's."""
+    ldx, dt = _rows(x, "x"), _dt(x)
+    tokens, k = x.shape
+    f, n = _mx_operand(w_codes, w_scales, k, fmt, "w", x.device)
+    with _On(x.device, stream) as s:
+        out, ldo = _mx_result(out, (tokens, n), dtype or x.dtype, x.device, "out")
+        _check(lib().bitopt_mx_linear(x.data_ptr(), dt, ldx, w_codes.data_ptr(), w_scales.data_ptr(), f, tokens, n, k,
+                                      out.data_ptr(), _dt(out), ldo, s))
+    return out
+
+
+def mx_linear_grad_input(dy, w_codes, w_scales, k: int, fmt: str = "e2m1", out=None, dtype=None, stream=None):
+    """dy W: the gradient of mx_linear's x from dy (tokens x n); dtype defaults to dy's."""
+    lddy, dt = _rows(dy, "dy"), _dt(dy)
+    tokens, n = dy.shape
+    f, rows = _mx_operand(w_codes, w_scales, k, fmt, "w", dy.device)
+    if rows != n:
+        raise ValueError(f"dy has {n} columns, w {rows} rows")
+    with _On(dy.device, stream) as s:
+        out, ldo = _mx_result(out, (tokens, k), dtype or dy.dtype, dy.device, "out")
+        _check(lib().bitopt_mx_linear_grad_input(dy.data_ptr(), dt, lddy, w_codes.data_ptr(), w_scales.data_ptr(), f,
+                                                 tokens, n, k, out.data_ptr(), _dt(out), ldo, s))
+    return out
+
+
+def mx_linear_grad_weight(dy, x_codes, x_scales, k: int, fmt: str = "e4m3", out=None, dtype=torch.float32,
+                          accumulate: bool = False, stream=None):
+    """dy^T x: the gradient of mx_linear's weights (n x k) from dy (tokens x n) and the
+    input kept as an MX matrix (tokens x k); `accumulate` adds it to `out`."""
+    lddy, dt = _rows(dy, "dy"), _dt(dy)
+    tokens, n = dy.shape
+    f, rows = _mx_operand(x_codes, x_scales, k, fmt, "x", dy.device)
+    if rows != tokens:
+        raise ValueError(f"dy has {tokens} rows, x {rows}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _On(dy.device, stream) as s:
+        out, ldo = _mx_result(out, (n, k), dtype, dy.device, "out")
+        _check(lib().bitopt_mx_linear_grad_weight(dy.data_ptr(), dt, lddy, x_codes.data_ptr(), x_scales.data_ptr(), f,
+                                                  tokens, n, k, out.data_ptr(), _dt(out), ldo, int(accumulate), s))
+    return out
+
+
+def swiglu_save8(gate, up, y=None, saved=None, stream=None):
+    """gate * sigmoid(gate) * up, and its inputs in 8 bits for swiglu_backward8: (y, saved),
+    saved = (gate_codes, gate_scales, up_codes, up_scales) in MX E4M3."""
+    ldg, dt = _rows(gate, "gate"), _dt(gate)
+    ldu = _rows(up, "up", gate.device)
+    if up.shape != gate.shape or up.dtype != gate.dtype:
+        raise ValueError("gate and up must have one shape and type")
+    rows, cols = gate.shape
+    with _On(gate.device, stream) as s:
+        y, ldy = _mx_result(y, (rows, cols), gate.dtype, gate.device, "y")
+        if y.dtype != gate.dtype:
+            raise TypeError(f"y: expected {gate.dtype}, got {y.dtype}")
+        gc, gs, uc, us = saved if saved is not None else (None,) * 4
+        gc, gs, _ = _mx_new(gc, gs, rows, cols, "e4m3", gate.device, "saved gate")
+        uc, us, _ = _mx_new(uc, us, rows, cols, "e4m3", gate.device, "saved up")
+        _check(lib().bitopt_swiglu_forward_mx8(gate.data_ptr(), up.data_ptr(), dt, rows, cols, ldg, ldu, y.data_ptr(),
+                                               ldy, gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr(), s))
+    return y, (gc, gs, uc, us)
+
+
+def swiglu_backward8(dy, saved, dgate=None, dup=None, stream=None):
+    """(dgate, dup) of swiglu_save8 from dy and what it saved."""
+    lddy, dt = _rows(dy, "dy"), _dt(dy)
+    rows, cols = dy.shape
+    gc, gs, uc, us = saved
+    for c, sc, name in ((gc, gs, "saved gate"), (uc, us, "saved up")):
+        if _mx_operand(c, sc, cols, "e4m3", name, dy.device)[1] != rows:
+            raise ValueError(f"{name}: expected {rows} rows")
+    with _On(dy.device, stream) as s:
+        dgate, lddg = _mx_result(dgate, (rows, cols), dy.dtype, dy.device, "dgate")
+        dup, lddu = _mx_result(dup, (rows, cols), dy.dtype, dy.device, "dup")
+        if dgate.dtype != dy.dtype or dup.dtype != dy.dtype:
+            raise TypeError(f"dgate and dup must be {dy.dtype}")
+        _check(lib().bitopt_swiglu_backward_mx8(dy.data_ptr(), dt, rows, cols, lddy, gc.data_ptr(), gs.data_ptr(),
+                                                uc.data_ptr(), us.data_ptr(), dgate.data_ptr(), lddg, dup.data_ptr(),
+                                                lddu, s))
+    return dgate, dup

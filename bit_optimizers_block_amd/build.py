@@ -31,7 +31,8 @@ FLAGS = [
 ]
 
 SOURCES = ["bitopt_api.cpp", "codec.hip", "step_adam.hip", "step_ademamix.hip",
-           "step_momentum.hip", "step_lion.hip", "step_rmsprop.hip", "step_adagrad.hip", "tensorwise.hip"]
+           "step_momentum.hip", "step_lion.hip", "step_rmsprop.hip", "step_adagrad.hip", "tensorwise.hip",
+           "mx_api.cpp", "mx_codec.hip", "mx_linear.hip", "mx_grad.hip", "mx_skinny.hip"]
 
 
 def _compile(src: str, extra=()) -> str:

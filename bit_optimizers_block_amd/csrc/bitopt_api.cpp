@@ -113,6 +113,17 @@ bitopt::StepScalars make_scalars(const bitopt_hparams& h, int32_t t) {
 
 namespace bitopt {
 
+int api_fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(code, "%s", buf);
+}
+
+int api_status(hipError_t e, const char* fn) { return device_status(e, fn); }
+
 // Compute units of each device, queried on first use.  Default groups per CU: 256
 // 4-wave groups, i.e. one tile per wave up to 64 M elements (B = 256) on 256 CUs, and
 // a grid stride beyond that, so very large launches stage the LDS codebooks once per

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "kernels.h"
+#include "mx.h"
 
 namespace bitopt {
 
@@ -27,6 +28,19 @@ int tensorwise_scratch_words();
 hipError_t launch_quantize(const CodecArgs& a, int dtype, int bs, hipStream_t s);
 hipError_t launch_dequantize(const CodecArgs& a, int dtype, int bs, hipStream_t s);
 
+// MX codec, SwiGLU with saved MX inputs, and the products of MX matrices.
+hipError_t launch_mx_quantize(const MxCodecArgs& a, int dtype, int fmt, hipStream_t s);
+hipError_t launch_mx_dequantize(const MxCodecArgs& a, int dtype, int fmt, hipStream_t s);
+hipError_t launch_swiglu_forward(const SwigluArgs& a, int dtype, hipStream_t s);
+hipError_t launch_swiglu_backward(const SwigluArgs& a, int dtype, hipStream_t s);
+hipError_t launch_mx_linear(const MxGemmArgs& g, int dtype, int fmt, hipStream_t s);
+hipError_t launch_mx_grad_input(const MxGemmArgs& g, int dtype, int fmt, hipStream_t s);
+hipError_t launch_mx_grad_weight(const MxGemmArgs& g, int dtype, int fmt, hipStream_t s);
+hipError_t launch_mx_matmul(const MxGemmArgs& g, int a_fmt, int b_fmt, hipStream_t s);
+constexpr int kMxSkinnyRows = 64;   // rows of A the skinny forms take
+hipError_t launch_mx_linear_skinny(const MxGemmArgs& g, int dtype, int fmt, hipStream_t s);
+hipError_t launch_mx_matmul_skinny(const MxGemmArgs& g, int a_fmt, int b_fmt, hipStream_t s);
+
 // Upper bound on the grid for the current device: compute units times the groups
 // per CU the step kernels are launched with (CU count queried once per device).
 // resident_per_cu > 0: that many groups per CU (a grid that is resident at once);
@@ -47,6 +61,10 @@ inline dim3 tile_grid(int64_t n, int64_t tile, int resident_per_cu = 0) {
     if (groups < 1) groups = 1;
     return dim3((unsigned)groups);
 }
+
+// Status of a C entry point: records the calling thread's error message.
+int api_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int api_status(hipError_t e, const char* fn);
 
 template <int OPT>
 hipError_t launch_step_family(const StepArgs& a, int dtype, int bs, bool quant, bool skip, bool unorm, hipStream_t s);

@@ -489,6 +489,106 @@ BITOPT_API int bitopt_step_multi(const bitopt_hparams* hp, int32_t step, const b
                                  int32_t count, const float* qmap1, const float* qmap2, void* workspace,
                                  int64_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- MX matrices
+ *
+ * Microscaled (MX) matrices: 4- and 8-bit weights and saved activations in blocks the
+ * matrix cores scale themselves, next to the 8-bit optimizer state above.  A matrix of
+ * rows x cols values is held as
+ *   codes    rows x bitopt_mx_code_bytes(cols, format) bytes
+ *   scales   rows x bitopt_mx_scale_bytes(cols) bytes
+ * row after row, both aligned to 16 bytes.  A block is 32 consecutive elements of a row;
+ * its scale byte s is the factor 2^(s-127), 255 is NaN.  Rows are padded to a multiple of
+ * 128 elements; padding codes and the scale bytes of padding blocks are zero, which
+ * bitopt_mx_quantize writes and the products rely on.
+ *   BITOPT_MX_E2M1   4 bits: sign, 2 exponent bits (bias 1), 1 fraction bit; 0, 0.5, 1,
+ *                    1.5, 2, 3, 4, 6 and their negatives.  Two codes a byte, the even
+ *                    column in the low half.
+ *   BITOPT_MX_E4M3   8 bits: sign, 4 exponent bits (bias 7), 3 fraction bits; largest
+ *                    value 448, smallest 2^-9; 0x7f and 0xff are NaN.
+ *
+ * Conventions of the calls below, besides those at the top of this file
+ *   - ldx, ldo, ... are the distances of consecutive rows in elements (at least the row's
+ *     length when there is more than one row); a row's elements are contiguous and need
+ *     only their own alignment.
+ *   - A size of zero gives a successful call: without results nothing is done, and a
+ *     product over no elements is zero.  Sizes above 2^30 give UNSUPPORTED.
+ *   - Inputs and results must not overlap, except that bitopt_swiglu_backward_mx8 may write
+ *     dgate or dup over dy when both have the same rows.
+ *   - No call needs a workspace, waits or allocates; every call may be captured into a HIP
+ *     graph and gives the same bits on every run.
+ */
+#define BITOPT_MX_E2M1 0
+#define BITOPT_MX_E4M3 1
+
+/* Bytes of codes and of scales in one row of an MX matrix of `cols` columns (-1: cols < 0
+ * or above 2^30, unknown format). */
+BITOPT_API int64_t bitopt_mx_code_bytes(int64_t cols, int32_t format);
+BITOPT_API int64_t bitopt_mx_scale_bytes(int64_t cols);
+
+/*
+ * Quantization to MX.  A block's scale is the smallest 2^e, e >= -127, whose product with
+ * the format's largest value is not below the block's largest |x| (no element saturates);
+ * its elements are x / 2^e rounded to nearest, ties to the even code, signs kept (also of
+ * zero).  A block that holds an infinity or a NaN gets scale 255 and zero codes: all of it
+ * decodes to NaN.
+ *   x   device, rows x cols of dtype
+ */
+BITOPT_API int bitopt_mx_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                  int32_t format, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* out[r][c] = element * scale, rounded to nearest-even into dtype (exact in fp32). */
+BITOPT_API int bitopt_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t format, int64_t rows,
+                                    int64_t cols, void* out, int32_t dtype, int64_t ldo, void* stream);
+
+/*
+ * Product of two MX matrices: out[m][n] = sum_k a[m][k] b[n][k], a m x k, b n x k, summed
+ * in fp32 and rounded once into out_dtype.  Two E2M1 operands run on the scaled matrix
+ * instructions.  With an E4M3 operand both are decoded to bf16 (exact while the scaled
+ * element is a normal number): the 8-bit matrix instructions align the products of a step
+ * to the largest one and drop what lies some 17 bits below it, which an fp32 result shows.
+ * Up to 64 rows of a take a form that reads b once and splits k over a workgroup's waves.
+ */
+BITOPT_API int bitopt_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_format,
+                                const uint8_t* b_codes, const uint8_t* b_scales, int32_t b_format, int64_t m, int64_t n,
+                                int64_t k, void* out, int32_t out_dtype, int64_t ldo, void* stream);
+
+/*
+ * The three products of a linear layer y = x W^T whose weights (n x k) or saved input
+ * (tokens x k) are MX matrices.  The 16-bit operand is fp16 or bf16 (fp32 gives
+ * UNSUPPORTED); the MX operand is decoded into that type, rounded to nearest-even -- exact
+ * in bf16 down to its subnormals; in fp16 a scaled element beyond 65504 is infinite.  Sums
+ * are fp32, rounded once into out_dtype.
+ *   forward       out[t][n] = sum_k x[t][k] W[n][k]   (up to 64 tokens: the form for
+ *                 decoding steps, bound by reading W once)
+ *   grad_input    dx[t][k]  = sum_n dy[t][n] W[n][k]
+ *   grad_weight   dw[n][k]  = sum_t dy[t][n] x[t][k]; accumulate != 0 adds it to dw
+ */
+BITOPT_API int bitopt_mx_linear(const void* x, int32_t dtype, int64_t ldx, const uint8_t* w_codes,
+                                const uint8_t* w_scales, int32_t format, int64_t tokens, int64_t n, int64_t k, void* out,
+                                int32_t out_dtype, int64_t ldo, void* stream);
+BITOPT_API int bitopt_mx_linear_grad_input(const void* dy, int32_t dtype, int64_t lddy, const uint8_t* w_codes,
+                                           const uint8_t* w_scales, int32_t format, int64_t tokens, int64_t n,
+                                           int64_t k, void* dx, int32_t out_dtype, int64_t lddx, void* stream);
+BITOPT_API int bitopt_mx_linear_grad_weight(const void* dy, int32_t dtype, int64_t lddy, const uint8_t* x_codes,
+                                            const uint8_t* x_scales, int32_t format, int64_t tokens, int64_t n,
+                                            int64_t k, void* dw, int32_t out_dtype, int64_t lddw, int32_t accumulate,
+                                            void* stream);
+
+/*
+ * SwiGLU whose inputs are kept for the backward pass in 8 bits (MX E4M3) instead of 16 or
+ * 32: with s = 1 / (1 + exp(-gate)),
+ *   forward    y = gate * s * up, and the codes and scales of gate and up
+ *   backward   dgate = dy * up * s * (1 + gate * (1 - s)),  dup = dy * gate * s
+ * with gate and up the values their codes stand for.  Arithmetic in fp32, rounded once.
+ */
+BITOPT_API int bitopt_swiglu_forward_mx8(const void* gate, const void* up, int32_t dtype, int64_t rows, int64_t cols,
+                                         int64_t ldg, int64_t ldu, void* y, int64_t ldy, uint8_t* gate_codes,
+                                         uint8_t* gate_scales, uint8_t* up_codes, uint8_t* up_scales, void* stream);
+BITOPT_API int bitopt_swiglu_backward_mx8(const void* dy, int32_t dtype, int64_t rows, int64_t cols, int64_t lddy,
+                                          const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                          const uint8_t* up_codes, const uint8_t* up_scales, void* dgate, int64_t lddg,
+                                          void* dup, int64_t lddu, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
