@@ -559,13 +559,17 @@ def step_multi(hp, step, tensors, qmap1=None, qmap2=None, workspace=None, stream
 
 
 # ------------------------------------------------------------------- MX matrices
+#
+# These calls run once per layer and token, so a call on the current device and stream
+# takes the short way: each argument is looked at once, and the stream's handle is read
+# without building a stream object.
 
 MX_FORMATS = {"e2m1": 0, "e4m3": 1}
 
 
 def mx_code_bytes(cols: int, fmt: str = "e2m1") -> int:
     """Bytes of codes in one row of an MX matrix: rows are padded to 128 elements."""
-    return (cols + 127) // 128 * (64 if _mx_format(fmt) == 0 else 128)
+    return (cols + 127) // 128 * (128 if _mx_format(fmt) else 64)
 
 
 def mx_scale_bytes(cols: int) -> int:
@@ -581,134 +585,153 @@ def _mx_format(fmt):
 
 
 def _rows(t, name, device=None):
-    """A device matrix with contiguous rows: (distance of its rows in elements)."""
+    """A device matrix with contiguous rows: (rows, columns, distance of rows in elements)."""
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
-    s = t.stride()
-    if s[1] != 1 and t.size(1) > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous (strides {s})")
-    if t.size(0) > 1 and s[0] < t.size(1):
-        raise ValueError(f"{name}: its rows overlap (strides {s})")
-    return s[0] if t.size(0) > 1 else t.size(1)
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous (strides {(ld, one)})")
+    if rows > 1:
+        if ld < cols:
+            raise ValueError(f"{name}: its rows overlap (strides {(ld, one)})")
+        return rows, cols, ld
+    return rows, cols, cols
 
 
 def _mx_operand(codes, scales, cols, fmt, name, device):
-    """Checks an MX matrix of `cols` columns; returns its rows."""
+    """Checks an MX matrix of `cols` columns; returns its format and rows."""
     f = _mx_format(fmt)
-    for t, what, width in ((codes, "codes", mx_code_bytes(cols, fmt)), (scales, "scales", mx_scale_bytes(cols))):
-        if t.dtype != torch.uint8:
+    pads = (cols + 127) // 128
+    rows = codes.size(0) if codes.dim() == 2 else -1
+    for t, what, width in ((codes, "codes", pads * (128 if f else 64)), (scales, "scales", pads * 4)):
+        if t.dtype is not torch.uint8:
             raise TypeError(f"{name} {what}: expected torch.uint8, got {t.dtype}")
-        if t.dim() != 2 or t.size(1) != width or not t.is_contiguous():
+        if tuple(t.shape) != (rows, width) or not t.is_contiguous():
             raise ValueError(f"{name} {what}: expected a contiguous matrix of {width} bytes a row for {cols} {fmt} "
-                             f"columns, got shape {tuple(t.shape)}")
+                             f"columns and as many rows of codes as of scales, got shape {tuple(t.shape)}")
         if not t.is_cuda or t.device != device:
             raise ValueError(f"{name} {what} must be on {device}")
-        if t.size(0) != codes.size(0):
-            raise ValueError(f"{name}: {codes.size(0)} rows of codes but {t.size(0)} of scales")
-    return f, codes.size(0)
+    return f, rows
 
 
-class _On:
-    """Makes `device` current, and `stream` the stream of the results allocated inside:
-    memory a caller's stream writes then belongs to that stream."""
-
-    def __init__(self, device, stream):
-        self._guards = []
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the arguments on {device}")
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self._guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+def _elsewhere(device, stream):
+    """None when work on `device` belongs on its current stream and it is the current device.
+    Otherwise a context that makes `device` (and `stream`, if given) current: results allocated
+    inside then belong to the stream that writes them."""
+    if stream is None:
+        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the arguments on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _mx_result(out, shape, dtype, device, name):
+def _current(device):
+    """Handle of the current stream of `device`."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _mx_result(out, rows, cols, dtype, device, name):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1]
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
-    return out, _rows(out, name, device)
+        if dtype not in DTYPES:
+            raise TypeError(f"unsupported dtype {dtype}")
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(out.shape)}")
+    return out, _rows(out, name, device)[2]
 
 
 def _mx_new(codes, scales, rows, cols, fmt, device, name):
+    """Result codes and scales: allocated, or the caller's, checked."""
+    f, pads = _mx_format(fmt), (cols + 127) // 128
     if codes is None:
-        codes = torch.empty((rows, mx_code_bytes(cols, fmt)), dtype=torch.uint8, device=device)
+        codes = torch.empty((rows, pads * (128 if f else 64)), dtype=torch.uint8, device=device)
+        if scales is None:
+            return codes, torch.empty((rows, pads * 4), dtype=torch.uint8, device=device), f
     if scales is None:
-        scales = torch.empty((rows, mx_scale_bytes(cols)), dtype=torch.uint8, device=device)
-    f, n = _mx_operand(codes, scales, cols, fmt, name, device)
-    if n != rows:
-        raise ValueError(f"{name}: expected {rows} rows of codes, got {n}")
+        scales = torch.empty((rows, pads * 4), dtype=torch.uint8, device=device)
+    if _mx_operand(codes, scales, cols, fmt, name, device)[1] != rows:
+        raise ValueError(f"{name}: expected {rows} rows of codes, got {codes.size(0)}")
     return codes, scales, f
 
 
 def mx_quantize(x, fmt: str = "e2m1", codes=None, scales=None, stream=None):
     """The MX form of a matrix: (codes, scales), blocks of 32 along its rows."""
-    ldx, dt = _rows(x, "x"), _dt(x)
-    rows, cols = x.shape
-    with _On(x.device, stream) as s:
-        codes, scales, f = _mx_new(codes, scales, rows, cols, fmt, x.device, "the result")
-        _check(lib().bitopt_mx_quantize(x.data_ptr(), dt, rows, cols, ldx, f, codes.data_ptr(), scales.data_ptr(), s))
+    rows, cols, ldx = _rows(x, "x")
+    dt, device = _dt(x), x.device
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_quantize(x, fmt, codes, scales)
+    codes, scales, f = _mx_new(codes, scales, rows, cols, fmt, device, "the result")
+    _check(lib().bitopt_mx_quantize(x.data_ptr(), dt, rows, cols, ldx, f, codes.data_ptr(), scales.data_ptr(),
+                                    _current(device)))
     return codes, scales
 
 
 def mx_dequantize(codes, scales, cols: int, fmt: str = "e2m1", out=None, dtype=torch.float32, stream=None):
     """The values of an MX matrix of `cols` columns."""
-    f, rows = _mx_operand(codes, scales, cols, fmt, "the input", codes.device)
-    with _On(codes.device, stream) as s:
-        out, ldo = _mx_result(out, (rows, cols), dtype, codes.device, "out")
-        _check(lib().bitopt_mx_dequantize(codes.data_ptr(), scales.data_ptr(), f, rows, cols, out.data_ptr(), _dt(out),
-                                          ldo, s))
+    device = codes.device
+    f, rows = _mx_operand(codes, scales, cols, fmt, "the input", device)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_dequantize(codes, scales, cols, fmt, out, dtype)
+    out, ldo = _mx_result(out, rows, cols, dtype, device, "out")
+    _check(lib().bitopt_mx_dequantize(codes.data_ptr(), scales.data_ptr(), f, rows, cols, out.data_ptr(), _dt(out), ldo,
+                                      _current(device)))
     return out
 
 
 def mx_matmul(a_codes, a_scales, b_codes, b_scales, k: int, a_fmt: str = "e2m1", b_fmt: str = "e2m1", out=None,
               dtype=torch.bfloat16, stream=None):
     """a b^T for MX matrices a (m x k) and b (n x k)."""
-    fa, m = _mx_operand(a_codes, a_scales, k, a_fmt, "a", a_codes.device)
-    fb, n = _mx_operand(b_codes, b_scales, k, b_fmt, "b", a_codes.device)
-    with _On(a_codes.device, stream) as s:
-        out, ldo = _mx_result(out, (m, n), dtype, a_codes.device, "out")
-        _check(lib().bitopt_mx_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(),
-                                      b_scales.data_ptr(), fb, m, n, k, out.data_ptr(), _dt(out), ldo, s))
+    device = a_codes.device
+    fa, m = _mx_operand(a_codes, a_scales, k, a_fmt, "a", device)
+    fb, n = _mx_operand(b_codes, b_scales, k, b_fmt, "b", device)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_matmul(a_codes, a_scales, b_codes, b_scales, k, a_fmt, b_fmt, out, dtype)
+    out, ldo = _mx_result(out, m, n, dtype, device, "out")
+    _check(lib().bitopt_mx_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(), b_scales.data_ptr(),
+                                  fb, m, n, k, out.data_ptr(), _dt(out), ldo, _current(device)))
     return out
 
 
 def mx_linear(x, w_codes, w_scales, fmt: str = "e2m1", out=None, dtype=None, stream=None):
     """x W^T for a 16-bit x (tokens x k) and MX weights W (n x k); dtype defaults to x's."""
-    ldx, dt = _rows(x, "x"), _dt(x)
-    tokens, k = x.shape
-    f, n = _mx_operand(w_codes, w_scales, k, fmt, "w", x.device)
-    with _On(x.device, stream) as s:
-        out, ldo = _mx_result(out, (tokens, n), dtype or x.dtype, x.device, "out")
-        _check(lib().bitopt_mx_linear(x.data_ptr(), dt, ldx, w_codes.data_ptr(), w_scales.data_ptr(), f, tokens, n, k,
-                                      out.data_ptr(), _dt(out), ldo, s))
+    tokens, k, ldx = _rows(x, "x")
+    dt, device = _dt(x), x.device
+    f, n = _mx_operand(w_codes, w_scales, k, fmt, "w", device)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_linear(x, w_codes, w_scales, fmt, out, dtype)
+    out, ldo = _mx_result(out, tokens, n, dtype or x.dtype, device, "out")
+    _check(lib().bitopt_mx_linear(x.data_ptr(), dt, ldx, w_codes.data_ptr(), w_scales.data_ptr(), f, tokens, n, k,
+                                  out.data_ptr(), _dt(out), ldo, _current(device)))
     return out
 
 
 def mx_linear_grad_input(dy, w_codes, w_scales, k: int, fmt: str = "e2m1", out=None, dtype=None, stream=None):
     """dy W: the gradient of mx_linear's x from dy (tokens x n); dtype defaults to dy's."""
-    lddy, dt = _rows(dy, "dy"), _dt(dy)
-    tokens, n = dy.shape
-    f, rows = _mx_operand(w_codes, w_scales, k, fmt, "w", dy.device)
+    tokens, n, lddy = _rows(dy, "dy")
+    dt, device = _dt(dy), dy.device
+    f, rows = _mx_operand(w_codes, w_scales, k, fmt, "w", device)
     if rows != n:
         raise ValueError(f"dy has {n} columns, w {rows} rows")
-    with _On(dy.device, stream) as s:
-        out, ldo = _mx_result(out, (tokens, k), dtype or dy.dtype, dy.device, "out")
-        _check(lib().bitopt_mx_linear_grad_input(dy.data_ptr(), dt, lddy, w_codes.data_ptr(), w_scales.data_ptr(), f,
-                                                 tokens, n, k, out.data_ptr(), _dt(out), ldo, s))
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_linear_grad_input(dy, w_codes, w_scales, k, fmt, out, dtype)
+    out, ldo = _mx_result(out, tokens, k, dtype or dy.dtype, device, "out")
+    _check(lib().bitopt_mx_linear_grad_input(dy.data_ptr(), dt, lddy, w_codes.data_ptr(), w_scales.data_ptr(), f,
+                                             tokens, n, k, out.data_ptr(), _dt(out), ldo, _current(device)))
     return out
 
 
@@ -716,54 +739,64 @@ def mx_linear_grad_weight(dy, x_codes, x_scales, k: int, fmt: str = "e4m3", out=
                           accumulate: bool = False, stream=None):
     """dy^T x: the gradient of mx_linear's weights (n x k) from dy (tokens x n) and the
     input kept as an MX matrix (tokens x k); `accumulate` adds it to `out`."""
-    lddy, dt = _rows(dy, "dy"), _dt(dy)
-    tokens, n = dy.shape
-    f, rows = _mx_operand(x_codes, x_scales, k, fmt, "x", dy.device)
+    tokens, n, lddy = _rows(dy, "dy")
+    dt, device = _dt(dy), dy.device
+    f, rows = _mx_operand(x_codes, x_scales, k, fmt, "x", device)
     if rows != tokens:
         raise ValueError(f"dy has {tokens} rows, x {rows}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with _On(dy.device, stream) as s:
-        out, ldo = _mx_result(out, (n, k), dtype, dy.device, "out")
-        _check(lib().bitopt_mx_linear_grad_weight(dy.data_ptr(), dt, lddy, x_codes.data_ptr(), x_scales.data_ptr(), f,
-                                                  tokens, n, k, out.data_ptr(), _dt(out), ldo, int(accumulate), s))
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_linear_grad_weight(dy, x_codes, x_scales, k, fmt, out, dtype, accumulate)
+    out, ldo = _mx_result(out, n, k, dtype, device, "out")
+    _check(lib().bitopt_mx_linear_grad_weight(dy.data_ptr(), dt, lddy, x_codes.data_ptr(), x_scales.data_ptr(), f,
+                                              tokens, n, k, out.data_ptr(), _dt(out), ldo, 1 if accumulate else 0,
+                                              _current(device)))
     return out
 
 
 def swiglu_save8(gate, up, y=None, saved=None, stream=None):
     """gate * sigmoid(gate) * up, and its inputs in 8 bits for swiglu_backward8: (y, saved),
     saved = (gate_codes, gate_scales, up_codes, up_scales) in MX E4M3."""
-    ldg, dt = _rows(gate, "gate"), _dt(gate)
-    ldu = _rows(up, "up", gate.device)
-    if up.shape != gate.shape or up.dtype != gate.dtype:
+    rows, cols, ldg = _rows(gate, "gate")
+    dt, device, dtype = _dt(gate), gate.device, gate.dtype
+    urows, ucols, ldu = _rows(up, "up", device)
+    if (urows, ucols) != (rows, cols) or up.dtype != dtype:
         raise ValueError("gate and up must have one shape and type")
-    rows, cols = gate.shape
-    with _On(gate.device, stream) as s:
-        y, ldy = _mx_result(y, (rows, cols), gate.dtype, gate.device, "y")
-        if y.dtype != gate.dtype:
-            raise TypeError(f"y: expected {gate.dtype}, got {y.dtype}")
-        gc, gs, uc, us = saved if saved is not None else (None,) * 4
-        gc, gs, _ = _mx_new(gc, gs, rows, cols, "e4m3", gate.device, "saved gate")
-        uc, us, _ = _mx_new(uc, us, rows, cols, "e4m3", gate.device, "saved up")
-        _check(lib().bitopt_swiglu_forward_mx8(gate.data_ptr(), up.data_ptr(), dt, rows, cols, ldg, ldu, y.data_ptr(),
-                                               ldy, gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr(), s))
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return swiglu_save8(gate, up, y, saved)
+    y, ldy = _mx_result(y, rows, cols, dtype, device, "y")
+    if y.dtype != dtype:
+        raise TypeError(f"y: expected {dtype}, got {y.dtype}")
+    gc, gs, uc, us = saved if saved is not None else (None, None, None, None)
+    gc, gs, _ = _mx_new(gc, gs, rows, cols, "e4m3", device, "saved gate")
+    uc, us, _ = _mx_new(uc, us, rows, cols, "e4m3", device, "saved up")
+    _check(lib().bitopt_swiglu_forward_mx8(gate.data_ptr(), up.data_ptr(), dt, rows, cols, ldg, ldu, y.data_ptr(), ldy,
+                                           gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr(), _current(device)))
     return y, (gc, gs, uc, us)
 
 
 def swiglu_backward8(dy, saved, dgate=None, dup=None, stream=None):
     """(dgate, dup) of swiglu_save8 from dy and what it saved."""
-    lddy, dt = _rows(dy, "dy"), _dt(dy)
-    rows, cols = dy.shape
+    rows, cols, lddy = _rows(dy, "dy")
+    dt, device, dtype = _dt(dy), dy.device, dy.dtype
     gc, gs, uc, us = saved
-    for c, sc, name in ((gc, gs, "saved gate"), (uc, us, "saved up")):
-        if _mx_operand(c, sc, cols, "e4m3", name, dy.device)[1] != rows:
-            raise ValueError(f"{name}: expected {rows} rows")
-    with _On(dy.device, stream) as s:
-        dgate, lddg = _mx_result(dgate, (rows, cols), dy.dtype, dy.device, "dgate")
-        dup, lddu = _mx_result(dup, (rows, cols), dy.dtype, dy.device, "dup")
-        if dgate.dtype != dy.dtype or dup.dtype != dy.dtype:
-            raise TypeError(f"dgate and dup must be {dy.dtype}")
-        _check(lib().bitopt_swiglu_backward_mx8(dy.data_ptr(), dt, rows, cols, lddy, gc.data_ptr(), gs.data_ptr(),
-                                                uc.data_ptr(), us.data_ptr(), dgate.data_ptr(), lddg, dup.data_ptr(),
-                                                lddu, s))
+    if _mx_operand(gc, gs, cols, "e4m3", "saved gate", device)[1] != rows or \
+            _mx_operand(uc, us, cols, "e4m3", "saved up", device)[1] != rows:
+        raise ValueError(f"what was saved does not have dy's {rows} rows")
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return swiglu_backward8(dy, saved, dgate, dup)
+    dgate, lddg = _mx_result(dgate, rows, cols, dtype, device, "dgate")
+    dup, lddu = _mx_result(dup, rows, cols, dtype, device, "dup")
+    if dgate.dtype != dtype or dup.dtype != dtype:
+        raise TypeError(f"dgate and dup must be {dtype}")
+    _check(lib().bitopt_swiglu_backward_mx8(dy.data_ptr(), dt, rows, cols, lddy, gc.data_ptr(), gs.data_ptr(),
+                                            uc.data_ptr(), us.data_ptr(), dgate.data_ptr(), lddg, dup.data_ptr(), lddu,
+                                            _current(device)))
     return dgate, dup

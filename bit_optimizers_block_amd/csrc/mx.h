@@ -180,12 +180,24 @@ template <int DT> __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x
                                                       0, 0);
 }
 
+// Four lane groups q hold dwords d[q] with bytes d[q][0..3]; afterwards group q holds
+// d[0..3][q].
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t d, int lane) {
+    const auto a = __builtin_amdgcn_permlane32_swap(d, d, false, false);
+    // a[0]: the dword of group q % 2, a[1]: of group 2 + q % 2; keep the byte pair q / 2 of both
+    const uint32_t pair = __builtin_amdgcn_perm(a[1], a[0], lane & 32 ? 0x07060302u : 0x05040100u);
+    const auto b = __builtin_amdgcn_permlane16_swap(pair, pair, false, false);
+    // b[0]: rows 0 and 2 of the pair, b[1]: rows 1 and 3; keep byte q % 2 of each row
+    return __builtin_amdgcn_perm(b[1], b[0], lane & 16 ? 0x07030501u : 0x06020400u);
+}
+
 // Scaled product of 16 x 128 E2M1 codes: lane l holds row l % 16 and block l / 16 of both
-// operands, and that block's scale in the low byte of sa / sb.
-__device__ __forceinline__ f32x4 mfma_e2m1(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+// operands, and that block's scale in byte BYTE of sa / sb.
+template <int BYTE>
+__device__ __forceinline__ f32x4 mfma_e2m1_at(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
     const i32x8 x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const i32x8 y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BYTE, (int)sa, BYTE, (int)sb);
 }
 
 // Four consecutive output elements of a row, columns n .. n+3 (those below N), with the
@@ -221,6 +233,30 @@ __device__ __forceinline__ void mx_store4(const MxGemmArgs& g, int64_t m, int n,
         if (n + 1 < g.N) gbl(o)[1] = (uint16_t)(lo >> 16);
         if (n + 2 < g.N) gbl(o)[2] = (uint16_t)hi;
     }
+}
+
+// Two neighbouring 16 x 16 result tiles of row m, columns n .. n+31: lane group q holds
+// columns 4 q .. + 3 of both.  16-bit results are exchanged between neighbouring groups
+// first, so a lane stores eight consecutive columns and a row gets whole 64-byte segments.
+__device__ __forceinline__ void mx_store_pair(const MxGemmArgs& g, int64_t m, int n, int q, f32x4 v, f32x4 w) {
+    if (g.out_dtype == kF32 || g.accumulate || n + 32 > g.N) {
+        if (m >= g.M) return;
+        if (n + 4 * q < g.N) mx_store4(g, m, n + 4 * q, v);
+        if (n + 16 + 4 * q < g.N) mx_store4(g, m, n + 16 + 4 * q, w);
+        return;
+    }
+    const bool bf = g.out_dtype == kBF16;
+    const uint32_t v0 = bf ? narrow2<kBF16>(v[0], v[1]) : narrow2<kF16>(v[0], v[1]);
+    const uint32_t v1 = bf ? narrow2<kBF16>(v[2], v[3]) : narrow2<kF16>(v[2], v[3]);
+    const uint32_t w0 = bf ? narrow2<kBF16>(w[0], w[1]) : narrow2<kF16>(w[0], w[1]);
+    const uint32_t w1 = bf ? narrow2<kBF16>(w[2], w[3]) : narrow2<kF16>(w[2], w[3]);
+    // odd groups of the first operand change places with even groups of the second
+    const auto a = __builtin_amdgcn_permlane16_swap(v0, w0, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(v1, w1, false, false);
+    // group q: tile q % 2, columns 8 (q / 2) .. + 7
+    if (m < g.M)
+        st16_a2(reinterpret_cast<uint16_t*>(g.out) + m * g.ldo + n + 16 * (q & 1) + 8 * (q >> 1),
+                u32x4{a[0], b[0], a[1], b[1]});
 }
 
 // Output tile of a workgroup.  Workgroups go round the 8 XCDs in turn, and each XCD has

@@ -10,6 +10,7 @@ using bitopt::api_status;
 using bitopt::MxGemmArgs;
 
 constexpr int64_t kMaxDim = int64_t{1} << 30;    // sizes, rounded up to a tile, are int32 in the kernels
+constexpr int64_t kMaxScaledK = int64_t{1} << 28; // a tile's scale offsets stay below 2^32
 
 bool valid_dtype(int32_t d) { return d == BITOPT_F32 || d == BITOPT_F16 || d == BITOPT_BF16; }
 bool valid_format(int32_t f) { return f == BITOPT_MX_E2M1 || f == BITOPT_MX_E4M3; }
@@ -119,6 +120,8 @@ int bitopt_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_
     BITOPT_TRY(check_dim(m, "m", fn));
     BITOPT_TRY(check_dim(n, "n", fn));
     BITOPT_TRY(check_dim(k, "k", fn));
+    if (k > kMaxScaledK)
+        return api_fail(BITOPT_ERR_UNSUPPORTED, "%s: k above %lld", fn, (long long)kMaxScaledK);
     if (m == 0 || n == 0) return api_status(hipSuccess, fn);
     BITOPT_TRY(check_tiles(m, n, fn));
     BITOPT_TRY(check_matrix(out, out_dtype, ldo, m, n, "out", fn));

@@ -14,6 +14,8 @@
 //   weight grad   dw[n][k] = sum_t dy[t][n] x[t][k]    A across, B across
 #pragma once
 
+#include <type_traits>
+
 #include "mx.h"
 
 namespace bitopt {
@@ -178,73 +180,90 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + wm + 16 * i + (lane & 15);
-        if (m >= g.M) continue;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int n = n0 + wn + 16 * j + (lane >> 4) * 4;
-            if (n < g.N) mx_store4(g, m, n, acc[i][j]);
-        }
+        for (int j = 0; j < FN; j += 2) mx_store_pair(g, m, n0 + wn + 16 * j, lane >> 4, acc[i][j], acc[i][j + 1]);
     }
 }
 
 // ------------------------------------------------------------------ both operands E2M1
 
-constexpr int kGemm4K = 256;    // contraction elements per LDS stage: 128 bytes of codes a row
+// Codes go from global memory straight to LDS in two stages of 256 contraction elements in
+// turn: 128 bytes of codes a row, a whole cache line (stages of 64 bytes a row fetched
+// lines twice).  A stage is multiplied in two steps of 128.  While the fragments of one step
+// are multiplied, those of the next are read from LDS; when the second step of a stage
+// begins, all of the stage is in registers and the stage after the next is asked for into
+// its buffer, two steps before it is needed.  That is one barrier per stage.  A wave's load
+// fills 1024 consecutive bytes of LDS, so the swizzle that spreads a fragment's rows over
+// the banks -- 16-byte chunk c of row r lies at chunk c ^ (r % 8) -- is applied to the source
+// address.
+//
+// Scales never touch LDS.  Lane (row i, group q) loads the four scale bytes of its row in
+// step q of a group of four steps; a byte transpose across the four lane groups leaves it
+// with the bytes of its own block in all four steps, and the matrix instruction selects
+// byte t itself.
 
-// Codes in the "along" image above (a 16-byte chunk is one block of 32); the eight scale
-// bytes of a row follow its operand's codes.
+constexpr int kGemm4K = 128;
+
+// Waits until at most N of the wave's global loads are outstanding and its LDS reads are
+// done, then for the workgroup.  The empty statements keep memory accesses on their side.
+template <int N> __device__ __forceinline__ void stage_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
-    constexpr int ROWS = BM + BN, CN = (ROWS * 8 + NT - 1) / NT, SN = (ROWS + NT - 1) / NT;
-    constexpr int CODES = ROWS * 128, STAGE = CODES + ROWS * 8;
-    static_assert(ROWS * 8 % NT == 0 && BM * 8 % NT == 0, "whole passes per operand");
+    constexpr int STAGE = (BM + BN) * 128, PASS_ROWS = NT / 8, LOADS = (BM + BN) / PASS_ROWS;
+    static_assert(BM % PASS_ROWS == 0 && BN % PASS_ROWS == 0 && PASS_ROWS % 8 == 0, "whole passes per operand");
     __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
 
     int tm, tn;
     mx_tile((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
-    const int padded = (int)mx_padded(g.K);
+    const int q = lane >> 4, li = lane & 15;
+    const int steps = (int)(mx_padded(g.K) / kGemm4K);
 
-    u32x4 raw[CN];
-    u32x2 rsc[SN];
-    auto load = [&](int k0) {
+    // this lane's source of pass i in stage 0: rows beyond the matrix repeat its last row
+    const int pr = tid >> 3, chunk = (tid & 7) ^ (pr & 7);
+    const uint8_t* src[LOADS];
 #pragma unroll
-        for (int i = 0; i < CN; ++i) {
-            const int idx = i * NT + tid, r = idx >> 3, k = k0 + (idx & 7) * kMxBlock;
-            const bool is_a = i * NT < BM * 8;      // a pass lies in one operand
-            const uint8_t* base = is_a ? reinterpret_cast<const uint8_t*>(g.a) : g.b;
-            const int64_t row = is_a ? min(m0 + r, g.M - 1) : min(n0 + r - BM, g.N - 1);
-            raw[i] = u32x4{0u, 0u, 0u, 0u};
-            if (k < padded)
-                raw[i] = *gbl(reinterpret_cast<const u32x4*>(base + row * (is_a ? g.a_row_bytes : g.b_row_bytes) + k / 2));
-        }
+    for (int i = 0; i < LOADS; ++i) {
+        const int r = i * PASS_ROWS + pr;
+        src[i] = i * PASS_ROWS < BM
+                     ? reinterpret_cast<const uint8_t*>(g.a) + (int64_t)min(m0 + r, g.M - 1) * g.a_row_bytes + chunk * 16
+                     : g.b + (int64_t)min(n0 + r - BM, g.N - 1) * g.b_row_bytes + chunk * 16;
+    }
+    // t: the stage's first step
+    auto issue = [&](int t, int buffer) {
+        // a last stage of one step: its second half repeats the first and is not multiplied
+        const int back = t + 1 < steps || chunk < 4 ? 0 : 64;
 #pragma unroll
-        for (int i = 0; i < SN; ++i) {
-            const int r = i * NT + tid;
-            rsc[i] = u32x2{0u, 0u};
-            if (ROWS % NT != 0 && r >= ROWS) continue;
-            const bool is_a = r < BM;
-            const uint8_t* p = is_a ? g.a_scales + min(m0 + r, g.M - 1) * g.a_row_scales
-                                    : g.b_scales + min(n0 + r - BM, g.N - 1) * g.b_row_scales;
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p + k0 / kMxBlock);
-            if (k0 < padded) rsc[i].x = gbl(w)[0];
-            if (k0 + 128 < padded) rsc[i].y = gbl(w)[1];
-        }
+        for (int i = 0; i < LOADS; ++i)
+            __builtin_amdgcn_global_load_lds((const BITOPT_GLOBAL void*)(src[i] + ((int64_t)t * 64 - back)),
+                                             (__attribute__((address_space(3))) void*)(lds + buffer * STAGE +
+                                                                                       i * NT * 16 + wave * 1024),
+                                             16, 0, 0);
     };
-    auto store = [&](char* to) {
+
+    // scale bytes of the fragments' rows, four steps at a time (rows of them hold a multiple of 4)
+    const uint8_t* sa0 = g.a_scales + (int64_t)m0 * g.a_row_scales;
+    const uint8_t* sb0 = g.b_scales + (int64_t)n0 * g.b_row_scales;
+    auto scales = [&](int step, uint32_t xa[FM], uint32_t xb[FN]) {
+        const int t = min(step + q, steps - 1);     // bytes of steps that are not taken are not looked at
 #pragma unroll
-        for (int i = 0; i < CN; ++i) {
-            const int idx = i * NT + tid, r = idx >> 3, c = idx & 7;
-            *reinterpret_cast<u32x4*>(to + r * 128 + ((c ^ (r & 7)) << 4)) = raw[i];
+        for (int i = 0; i < FM; ++i) {
+            const uint32_t r = (uint32_t)min(wm + 16 * i + li, g.M - 1 - m0);
+            xa[i] = *gbl(reinterpret_cast<const uint32_t*>(sa0 + (r * (uint32_t)g.a_row_scales + 4 * t)));
         }
 #pragma unroll
-        for (int i = 0; i < SN; ++i) {
-            const int r = i * NT + tid;
-            if (ROWS % NT != 0 && r >= ROWS) continue;
-            *reinterpret_cast<u32x2*>(to + CODES + r * 8) = rsc[i];
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t r = (uint32_t)min(wn + 16 * j + li, g.N - 1 - n0);
+            xb[j] = *gbl(reinterpret_cast<const uint32_t*>(sb0 + (r * (uint32_t)g.b_row_scales + 4 * t)));
         }
     };
 
@@ -254,54 +273,62 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int q = lane >> 4, li = lane & 15;
-    const int steps = (padded + kGemm4K - 1) / kGemm4K;
-    load(0);
-    store(lds);
-    __syncthreads();
-    for (int t = 0; t < steps; ++t) {
-        const char* cur = lds + (t & 1) * STAGE;
-        if (t + 1 < steps) load((t + 1) * kGemm4K);
-        u32x2 xa[FM], xb[FN];
+    struct Fragments {
+        u32x4 a[FM], b[FN];
+    };
+    auto read = [&](int buffer, int half, Fragments& f) {
+        const char* cur = lds + buffer * STAGE + li * 128 + (((half * 4 + q) ^ (li & 7)) << 4);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-            xa[i] = *reinterpret_cast<const u32x2*>(cur + CODES + (wm + 16 * i + li) * 8) >> (8 * q);
+        for (int j = 0; j < FN; ++j) f.b[j] = *reinterpret_cast<const u32x4*>(cur + (BM + wn + 16 * j) * 128);
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-            xb[j] = *reinterpret_cast<const u32x2*>(cur + CODES + (BM + wn + 16 * j + li) * 8) >> (8 * q);
+        for (int i = 0; i < FM; ++i) f.a[i] = *reinterpret_cast<const u32x4*>(cur + (wm + 16 * i) * 128);
+    };
+
+    if (steps > 0) issue(0, 0);
+    if (steps > 2) issue(2, 1);
+    uint32_t xa[FM], xb[FN], ya[FM], yb[FN];
+    Fragments even, odd;
+    if (steps > 0) {
+        scales(0, xa, xb);
+        stage_barrier<0>();
+        read(0, 0, even);
+    }
+    for (int t0 = 0; t0 < steps; t0 += 4) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            u32x4 fa[FM], fb[FN];
+        for (int i = 0; i < FM; ++i) ya[i] = transpose_bytes(xa[i], lane);
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int r = wm + 16 * i + li;
-                fa[i] = *reinterpret_cast<const u32x4*>(cur + r * 128 + (((ks * 4 + q) ^ (r & 7)) << 4));
+        for (int j = 0; j < FN; ++j) yb[j] = transpose_bytes(xb[j], lane);
+        auto step = [&](auto byte, const Fragments& cur, Fragments& next) {
+            constexpr int B = decltype(byte)::value;
+            const int t = t0 + B;
+            if (t >= steps) return;
+            if constexpr (B & 1) {
+                // the next stage has to be there, and every wave to have read this one
+                stage_barrier<0>();
+                if (t + 3 < steps) issue(t + 3, B >> 1);
+                if constexpr (B == 1) scales(t0 + 4, xa, xb);
             }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int r = BM + wn + 16 * j + li;
-                fb[j] = *reinterpret_cast<const u32x4*>(cur + r * 128 + (((ks * 4 + q) ^ (r & 7)) << 4));
-            }
+            read((B + 1) / 2 % 2, (B + 1) % 2, next);      // after the last step: not looked at
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = mfma_e2m1(fb[j], fa[i], acc[i][j], ks ? xb[j].y : xb[j].x, ks ? xa[i].y : xa[i].x);
-        }
-        if (t + 1 < steps) {
-            store(lds + ((t + 1) & 1) * STAGE);
-            __syncthreads();
-        }
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma_e2m1_at<B>(cur.b[j], cur.a[i], acc[i][j], yb[j], ya[i]);
+#pragma unroll
+            for (int r = 0; r < FM + FN; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                     // one LDS read
+                __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / (FM + FN), 0);   // its share of products
+            }
+        };
+        step(std::integral_constant<int, 0>{}, even, odd);
+        step(std::integral_constant<int, 1>{}, odd, even);
+        step(std::integral_constant<int, 2>{}, even, odd);
+        step(std::integral_constant<int, 3>{}, odd, even);
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + wm + 16 * i + li;
-        if (m >= g.M) continue;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int n = n0 + wn + 16 * j + q * 4;
-            if (n < g.N) mx_store4(g, m, n, acc[i][j]);
-        }
+        for (int j = 0; j < FN; j += 2) mx_store_pair(g, m, n0 + wn + 16 * j, q, acc[i][j], acc[i][j + 1]);
     }
 }
 
