@@ -10,7 +10,7 @@ using bitopt::api_status;
 using bitopt::MxGemmArgs;
 
 constexpr int64_t kMaxDim = int64_t{1} << 30;    // sizes, rounded up to a tile, are int32 in the kernels
-constexpr int64_t kMaxScaledK = int64_t{1} << 28; // a tile's scale offsets stay below 2^32
+constexpr int64_t kMaxScaledK = int64_t{1} << 24;  // offsets within a tile of 256 rows stay below 2^32
 
 bool valid_dtype(int32_t d) { return d == BITOPT_F32 || d == BITOPT_F16 || d == BITOPT_BF16; }
 bool valid_format(int32_t f) { return f == BITOPT_MX_E2M1 || f == BITOPT_MX_E4M3; }

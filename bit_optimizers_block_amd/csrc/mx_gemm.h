@@ -28,13 +28,13 @@ constexpr bool mx_is_4bit(int s) { return s == kAlongE2M1 || s == kAcrossE2M1; }
 
 constexpr int kGemmK = 64;      // contraction elements per LDS stage of the 16-bit product
 
-// One operand's way from global memory to LDS: R rows (columns, if across) by kGemmK
-// contraction elements of 16 bits.
+// One operand's way from global memory through registers to LDS: R rows (columns, if
+// across) by kGemmK contraction elements of 16 bits.
 //
 // LDS image, along: R rows of 128 bytes; 16-byte chunk c of row r is stored at chunk
 // c ^ (r & 7), so the 16 rows of a fragment read fall on different banks.  Across: kGemmK
-// rows of 2R bytes; 32-byte segment s of row k is stored at segment s ^ f(k), f of the four
-// rows and two row groups that one transpose read touches, for the same reason.
+// rows of 2R bytes and 32 of padding, so the four rows of a transpose read do (a swizzle of
+// the segments does the same, but costs a register of addresses for every fragment).
 template <int DT, int SRC, int R, int NT> struct MxStage {
     static constexpr bool along = mx_is_along(SRC), codes = mx_is_codes(SRC), four = mx_is_4bit(SRC);
     // elements per thread item: one 16-byte load
@@ -42,23 +42,64 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     static constexpr int PER_ROW = (along ? kGemmK : R) / EL;
     static constexpr int ITEMS = PER_ROW * (along ? R : kGemmK);
     static constexpr int N = (ITEMS + NT - 1) / NT;
-    static constexpr int BYTES = R * kGemmK * 2;
+    static constexpr int PIECES = N * EL / 8;           // 16-byte LDS writes of a thread
+    static constexpr int PITCH = along ? kGemmK * 2 : R * 2 + 32;
+    static constexpr int BYTES = PITCH * (along ? R : kGemmK);
     static_assert(PER_ROW >= 1, "tile narrower than an item");
 
+    // Offsets of this thread's items from the tile's first byte of a stage, where they fit 32
+    // bits; otherwise, and where a stage reaches over an edge, load_any() is taken.  Across,
+    // item i lies a uniform distance behind item 0; along, rows beyond the last repeat it.
+    static constexpr int OFFS = along ? N : 1;
+    static constexpr int ROWS = NT / PER_ROW;           // memory rows from an item to the next
+    static_assert(along || N == 1 || NT % PER_ROW == 0, "items of a thread in one column");
+    uint32_t off[OFFS], soff[codes ? OFFS : 1];
     u32x4 raw[N];
-    float scale[codes ? N : 1];
+    uint32_t scale[codes ? N : 1];
 
-    static __device__ __forceinline__ int swizzle(int k) { return (k & 3) | (R >= 128 ? ((k >> 3) & 1) << 2 : 0); }
-
-    // r0: first row (column) of the tile, k0: first contraction element.
-    __device__ __forceinline__ void load(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int rows, int K,
-                                         int r0, int k0, int tid) {
+    // rows: the operand's rows (columns, if across); r0: the tile's first
+    __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int r0, int tid) {
+#pragma unroll
+        for (int i = 0; i < OFFS; ++i) {
+            const int idx = min(i * NT + tid, ITEMS - 1);
+            const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
+            const uint32_t row = along ? (uint32_t)min(a, rows - 1 - r0) : (uint32_t)a;
+            off[i] = row * (uint32_t)(codes ? ld : 2 * ld) + (codes ? (four ? b / 2 : b) : 2 * b);
+            if constexpr (codes) soff[i] = row * (uint32_t)ld_sc + b / kMxBlock;
+        }
+    }
+    // Whether the stage from k0 lies inside the operand and its offsets fit (wave-uniform).
+    static __device__ __forceinline__ bool inside(int64_t ld, int rows, int K, int r0, int k0) {
+        if (ld >= (1 << 22)) return false;
+        if (along) return codes || k0 + kGemmK <= K;
+        return k0 + kGemmK <= K && r0 + R <= (codes ? (int)mx_padded(rows) : rows);
+    }
+    __device__ __forceinline__ void load_inside(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int r0,
+                                                int k0) {
+        const int64_t row = along ? r0 : k0, col = along ? k0 : r0;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + row * (codes ? ld : 2 * ld) +
+                           (codes ? (four ? col / 2 : col) : 2 * col);
+        const int64_t next = along ? 0 : ROWS * (codes ? ld : 2 * ld);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint8_t* q = p + i * next + off[along ? i : 0];
+            if constexpr (codes) raw[i] = *gbl(reinterpret_cast<const u32x4*>(q));
+            else raw[i] = ld16_a2(q);
+        }
+        if constexpr (codes) {
+            const uint8_t* s = sc + row * ld_sc + col / kMxBlock;
+#pragma unroll
+            for (int i = 0; i < N; ++i) scale[i] = gbl(s + (along ? 0 : i * ROWS * ld_sc))[soff[along ? i : 0]];
+        }
+    }
+    __device__ __forceinline__ void load_any(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int rows,
+                                             int K, int r0, int k0, int tid) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int idx = i * NT + tid;
             const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
             raw[i] = u32x4{0u, 0u, 0u, 0u};
-            if constexpr (codes) scale[i] = 0.0f;
+            if constexpr (codes) scale[i] = 0u;
             if (ITEMS % NT != 0 && idx >= ITEMS) continue;
             // memory row and first element of the item
             const int64_t row = along ? min(r0 + a, rows - 1) : k0 + a;
@@ -74,30 +115,29 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
                 if (col < width && (along || row < K)) {
                     raw[i] = *gbl(reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(base) + row * ld +
                                                                 (four ? col / 2 : col)));
-                    scale[i] = mx_scale_f32(gbl(sc)[row * ld_sc + col / kMxBlock]);
+                    scale[i] = gbl(sc)[row * ld_sc + col / kMxBlock];
                 }
             }
         }
     }
+    __device__ __forceinline__ void load(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int rows, int K,
+                                         int r0, int k0, int tid) {
+        if (inside(ld, rows, K, r0, k0)) load_inside(base, ld, sc, ld_sc, r0, k0);
+        else load_any(base, ld, sc, ld_sc, rows, K, r0, k0, tid);
+    }
 
-    __device__ __forceinline__ void store(char* lds, int tid) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int idx = i * NT + tid;
-            const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
-            if (ITEMS % NT != 0 && idx >= ITEMS) continue;
-#pragma unroll
-            for (int h = 0; h < EL / 8; ++h) {
-                u32x4 v;
-                if constexpr (!codes) v = raw[i];
-                else if constexpr (four) v = mx_half8_e2m1<DT>(raw[i][h], scale[i]);
-                else v = mx_half8_e4m3<DT>(raw[i][2 * h], raw[i][2 * h + 1], scale[i]);
-                const int c = b / 8 + h;            // 16-byte chunk of the row
-                const int at = along ? a * (kGemmK * 2) + ((c ^ (a & 7)) << 4)
-                                     : a * (R * 2) + (((c >> 1) ^ swizzle(a)) << 5) + ((c & 1) << 4);
-                *reinterpret_cast<u32x4*>(lds + at) = v;
-            }
-        }
+    // Write p of this thread: eight elements, decoded on the way.
+    __device__ __forceinline__ void store(char* lds, int tid, int p) const {
+        const int i = p / (EL / 8), h = p % (EL / 8);
+        const int idx = i * NT + tid;
+        const int a = idx / PER_ROW, c = idx % PER_ROW * (EL / 8) + h;      // row, 16-byte chunk of it
+        if (ITEMS % NT != 0 && idx >= ITEMS) return;
+        u32x4 v;
+        if constexpr (!codes) v = raw[i];
+        else if constexpr (four) v = mx_half8_e2m1<DT>(raw[i][h], mx_scale_f32(scale[i]));
+        else v = mx_half8_e4m3<DT>(raw[i][2 * h], raw[i][2 * h + 1], mx_scale_f32(scale[i]));
+        const int at = a * PITCH + ((along ? c ^ (a & 7) : c) << 4);
+        *reinterpret_cast<u32x4*>(lds + at) = v;
     }
 
     // Fragment of rows r .. r+15 and contraction elements 32 ks .. 32 ks + 31: lane l holds
@@ -106,21 +146,34 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
         const int i = lane & 15, q = lane >> 4;
         if constexpr (along) {
             const int row = r + i;
-            return *reinterpret_cast<const u32x4*>(lds + row * (kGemmK * 2) + (((ks * 4 + q) ^ (row & 7)) << 4));
+            return *reinterpret_cast<const u32x4*>(lds + row * PITCH + (((ks * 4 + q) ^ (i & 7)) << 4));
         } else {
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
             const int k = ks * 32 + q * 8 + (i >> 2);
-            const char* p = lds + k * (R * 2) + (((r >> 4) ^ swizzle(k)) << 5) + ((i & 3) << 3);
+            const char* p = lds + k * PITCH + 2 * r + ((i & 3) << 3);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (R * 2)));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * PITCH));
             const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
             return u32x4{a.x, a.y, b.x, b.y};
         }
     }
 };
 
-// Workgroup tile BM x BN, wave tile WM x WN.
+// Waits for the wave's LDS accesses, then for the workgroup; global loads stay in flight.
+// The empty statements keep memory accesses on their side.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Workgroup tile BM x BN, wave tile WM x WN.  Two LDS buffers of one stage (64 contraction
+// elements, two steps of 32).  While the fragments of a step are multiplied, those of the
+// next are read.  When the second step of a stage begins, all of the stage is in registers:
+// its buffer takes the stage after the next, whose loads were sent two steps before, and the
+// loads of the stage after that are sent.  One barrier per stage.
 template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
@@ -132,50 +185,77 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
     int tm, tn;
     mx_tile((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
     const int64_t lda = SA::codes ? g.a_row_bytes : g.lda;
+    const int stages = (g.K + kGemmK - 1) / kGemmK;
 
     SA sa;
     SB sb;
+    sa.init(lda, g.a_row_scales, g.M, m0, tid);
+    sb.init(g.b_row_bytes, g.b_row_scales, g.N, n0, tid);
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int steps = (g.K + kGemmK - 1) / kGemmK;
-    sa.load(g.a, lda, g.a_scales, g.a_row_scales, g.M, g.K, m0, 0, tid);
-    sb.load(g.b, g.b_row_bytes, g.b_scales, g.b_row_scales, g.N, g.K, n0, 0, tid);
-    sa.store(lds, tid);
-    sb.store(lds + SA::BYTES, tid);
-    __syncthreads();
-    for (int t = 0; t < steps; ++t) {
-        const char* cur = lds + (t & 1) * STAGE;
-        if (t + 1 < steps) {
-            sa.load(g.a, lda, g.a_scales, g.a_row_scales, g.M, g.K, m0, (t + 1) * kGemmK, tid);
-            sb.load(g.b, g.b_row_bytes, g.b_scales, g.b_row_scales, g.N, g.K, n0, (t + 1) * kGemmK, tid);
-        }
+    auto load = [&](int s) {
+        if (s >= stages) return;
+        sa.load(g.a, lda, g.a_scales, g.a_row_scales, g.M, g.K, m0, s * kGemmK, tid);
+        sb.load(g.b, g.b_row_bytes, g.b_scales, g.b_row_scales, g.N, g.K, n0, s * kGemmK, tid);
+    };
+    constexpr int P = SA::PIECES + SB::PIECES;
+    auto store = [&](int buffer, int p) {
+        if (p < SA::PIECES) sa.store(lds + buffer * STAGE, tid, p);
+        else sb.store(lds + buffer * STAGE + SA::BYTES, tid, p - SA::PIECES);
+    };
+    struct Fragments {
+        u32x4 a[FM], b[FN];
+    };
+    // fragment r of a step: B's, then A's
+    constexpr int G = FM + FN;
+    auto read = [&](int buffer, int ks, Fragments& f, int r) {
+        if (r < FN) f.b[r] = SB::fragment(lds + buffer * STAGE + SA::BYTES, wn + 16 * r, ks, lane);
+        else f.a[r - FN] = SA::fragment(lds + buffer * STAGE, wm + 16 * (r - FN), ks, lane);
+    };
+    // B first: a lane then holds four consecutive columns of one output row
+    auto multiply = [&](const Fragments& f) {
 #pragma unroll
-        for (int ks = 0; ks < kGemmK / 32; ++ks) {
-            u32x4 fa[FM], fb[FN];
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int i = 0; i < FM; ++i) fa[i] = SA::fragment(cur, wm + 16 * i, ks, lane);
+            for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<DT>(f.b[j], f.a[i], acc[i][j]);
+    };
+
+    if (stages > 0) {
+        load(0);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) fb[j] = SB::fragment(cur + SA::BYTES, wn + 16 * j, ks, lane);
-            // B first: a lane then holds four consecutive columns of one output row
+        for (int p = 0; p < P; ++p) store(0, p);
+        load(1);
+        lds_barrier();
+    }
+    for (int s0 = 0; s0 < stages; s0 += 2) {
+        auto stage = [&](auto buffer) {
+            constexpr int B = decltype(buffer)::value;
+            const int s = s0 + B;
+            if (s >= stages) return;
+            Fragments f;
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int r = 0; r < G; ++r) read(B, 0, f, r);
+            multiply(f);
+            Fragments h;
 #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
-        }
-        if (t + 1 < steps) {
-            // the other buffer was last read before the barrier that ended step t - 1
-            char* next = lds + ((t + 1) & 1) * STAGE;
-            sa.store(next, tid);
-            sb.store(next + SA::BYTES, tid);
-            __syncthreads();
-        }
+            for (int r = 0; r < G; ++r) {
+                read(B, 1, h, r);
+#pragma unroll
+                for (int p = r * P / G; p < (r + 1) * P / G; ++p) store(B ^ 1, p);
+            }
+            multiply(h);
+            load(s + 2);
+            lds_barrier();
+        };
+        stage(std::integral_constant<int, 0>{});
+        stage(std::integral_constant<int, 1>{});
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -197,10 +277,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // the banks -- 16-byte chunk c of row r lies at chunk c ^ (r % 8) -- is applied to the source
 // address.
 //
-// Scales never touch LDS.  Lane (row i, group q) loads the four scale bytes of its row in
-// step q of a group of four steps; a byte transpose across the four lane groups leaves it
-// with the bytes of its own block in all four steps, and the matrix instruction selects
-// byte t itself.
+// Scales come by the same direct loads, eight steps (32 bytes a row) at a time.  Lane (row
+// i, group q) reads the four scale bytes of its row in step q of four; a byte transpose
+// across the four lane groups leaves it with the bytes of its own block in all four steps,
+// and the matrix instruction selects byte t itself.  (Loaded from global memory in that
+// pattern, 64 separate dwords an instruction, scales were two thirds of the cache's
+// accesses: 8192 x 8192 x 8192 took 347 us.)
 
 constexpr int kGemm4K = 128;
 
@@ -217,8 +299,10 @@ template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
     constexpr int STAGE = (BM + BN) * 128, PASS_ROWS = NT / 8, LOADS = (BM + BN) / PASS_ROWS;
+    constexpr int SCALES = (BM + BN) * 32, SCALE_LOADS = SCALES / (NT * 4);
     static_assert(BM % PASS_ROWS == 0 && BN % PASS_ROWS == 0 && PASS_ROWS % 8 == 0, "whole passes per operand");
-    __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
+    static_assert(SCALES % (NT * 4) == 0 && BM * 8 % NT == 0, "whole passes per operand");
+    __shared__ __attribute__((aligned(16))) char lds[2 * STAGE + 2 * SCALES];
 
     int tm, tn;
     mx_tile((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn);
@@ -228,43 +312,60 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
     const int q = lane >> 4, li = lane & 15;
     const int steps = (int)(mx_padded(g.K) / kGemm4K);
 
-    // this lane's source of pass i in stage 0: rows beyond the matrix repeat its last row
+    // this lane's part of pass i, from the tile's first byte of a stage: rows beyond the
+    // matrix repeat its last row
     const int pr = tid >> 3, chunk = (tid & 7) ^ (pr & 7);
-    const uint8_t* src[LOADS];
+    const uint8_t* a_stage = reinterpret_cast<const uint8_t*>(g.a) + (int64_t)m0 * g.a_row_bytes;
+    const uint8_t* b_stage = g.b + (int64_t)n0 * g.b_row_bytes;
+    uint32_t off[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const int r = i * PASS_ROWS + pr;
-        src[i] = i * PASS_ROWS < BM
-                     ? reinterpret_cast<const uint8_t*>(g.a) + (int64_t)min(m0 + r, g.M - 1) * g.a_row_bytes + chunk * 16
-                     : g.b + (int64_t)min(n0 + r - BM, g.N - 1) * g.b_row_bytes + chunk * 16;
+        off[i] = (i * PASS_ROWS < BM ? (uint32_t)min(r, g.M - 1 - m0) * (uint32_t)g.a_row_bytes
+                                     : (uint32_t)min(r - BM, g.N - 1 - n0) * (uint32_t)g.b_row_bytes) + chunk * 16;
     }
-    // t: the stage's first step
-    auto issue = [&](int t, int buffer) {
-        // a last stage of one step: its second half repeats the first and is not multiplied
-        const int back = t + 1 < steps || chunk < 4 ? 0 : 64;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds((const BITOPT_GLOBAL void*)(src[i] + ((int64_t)t * 64 - back)),
-                                             (__attribute__((address_space(3))) void*)(lds + buffer * STAGE +
-                                                                                       i * NT * 16 + wave * 1024),
-                                             16, 0, 0);
+    auto issue = [&](int i, int buffer, uint32_t back) {
+        __builtin_amdgcn_global_load_lds(
+            (const BITOPT_GLOBAL void*)((i * PASS_ROWS < BM ? a_stage : b_stage) + (off[i] - back)),
+            (__attribute__((address_space(3))) void*)(lds + buffer * STAGE + i * NT * 16 + wave * 1024), 16, 0, 0);
+    };
+    // The source moves on while there are stages; after the last, loads repeat it into buffers
+    // that are not read.  Of a last stage of one step the second half repeats the first.
+    const int last = (steps - 1) & ~1;
+    auto back = [&](int t) { return (steps & 1) && t >= last && chunk >= 4 ? 64u : 0u; };
+    auto advance = [&](int t) {
+        a_stage += t < last ? 128 : 0;
+        b_stage += t < last ? 128 : 0;
     };
 
-    // scale bytes of the fragments' rows, four steps at a time (rows of them hold a multiple of 4)
+    // scale bytes of eight steps: lane l of a pass takes step l % 8 of row l / 8
     const uint8_t* sa0 = g.a_scales + (int64_t)m0 * g.a_row_scales;
     const uint8_t* sb0 = g.b_scales + (int64_t)n0 * g.b_row_scales;
-    auto scales = [&](int step, uint32_t xa[FM], uint32_t xb[FN]) {
-        const int t = min(step + q, steps - 1);     // bytes of steps that are not taken are not looked at
+    uint32_t soff[SCALE_LOADS];
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const uint32_t r = (uint32_t)min(wm + 16 * i + li, g.M - 1 - m0);
-            xa[i] = *gbl(reinterpret_cast<const uint32_t*>(sa0 + (r * (uint32_t)g.a_row_scales + 4 * t)));
-        }
+    for (int i = 0; i < SCALE_LOADS; ++i) {
+        const int r = i * PASS_ROWS + pr;
+        soff[i] = i * PASS_ROWS < BM ? (uint32_t)min(r, g.M - 1 - m0) * (uint32_t)g.a_row_scales
+                                     : (uint32_t)min(r - BM, g.N - 1 - n0) * (uint32_t)g.b_row_scales;
+    }
+    auto issue_scales = [&](int t, int buffer) {
+        const uint32_t o = 4u * (uint32_t)min(t + (tid & 7), steps - 1);    // beyond the last step: not looked at
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const uint32_t r = (uint32_t)min(wn + 16 * j + li, g.N - 1 - n0);
-            xb[j] = *gbl(reinterpret_cast<const uint32_t*>(sb0 + (r * (uint32_t)g.b_row_scales + 4 * t)));
-        }
+        for (int i = 0; i < SCALE_LOADS; ++i)
+            __builtin_amdgcn_global_load_lds(
+                (const BITOPT_GLOBAL void*)((i * PASS_ROWS < BM ? sa0 : sb0) + (soff[i] + o)),
+                (__attribute__((address_space(3))) void*)(lds + 2 * STAGE + buffer * SCALES + i * NT * 4 + wave * 256), 4, 0,
+                0);
+    };
+    // four steps from t
+    auto scales = [&](int t, uint32_t ya[FM], uint32_t yb[FN]) {
+        const char* cur = lds + 2 * STAGE + (t >> 3 & 1) * SCALES + li * 32 + (t & 4) * 4 + q * 4;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            ya[i] = transpose_bytes(*reinterpret_cast<const uint32_t*>(cur + (wm + 16 * i) * 32), lane);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            yb[j] = transpose_bytes(*reinterpret_cast<const uint32_t*>(cur + (BM + wn + 16 * j) * 32), lane);
     };
 
     f32x4 acc[FM][FN];
@@ -276,47 +377,60 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
     struct Fragments {
         u32x4 a[FM], b[FN];
     };
-    auto read = [&](int buffer, int half, Fragments& f) {
+    // fragment r of the step: B's, then A's
+    auto read = [&](int buffer, int half, Fragments& f, int r) {
         const char* cur = lds + buffer * STAGE + li * 128 + (((half * 4 + q) ^ (li & 7)) << 4);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) f.b[j] = *reinterpret_cast<const u32x4*>(cur + (BM + wn + 16 * j) * 128);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) f.a[i] = *reinterpret_cast<const u32x4*>(cur + (wm + 16 * i) * 128);
+        if (r < FN) f.b[r] = *reinterpret_cast<const u32x4*>(cur + (BM + wn + 16 * r) * 128);
+        else f.a[r - FN] = *reinterpret_cast<const u32x4*>(cur + (wm + 16 * (r - FN)) * 128);
     };
 
-    if (steps > 0) issue(0, 0);
-    if (steps > 2) issue(2, 1);
-    uint32_t xa[FM], xb[FN], ya[FM], yb[FN];
     Fragments even, odd;
     if (steps > 0) {
-        scales(0, xa, xb);
+        issue_scales(0, 0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) issue(i, s, back(2 * s));
+            advance(2 * s);
+        }
         stage_barrier<0>();
-        read(0, 0, even);
+#pragma unroll
+        for (int r = 0; r < FM + FN; ++r) read(0, 0, even, r);
     }
     for (int t0 = 0; t0 < steps; t0 += 4) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) ya[i] = transpose_bytes(xa[i], lane);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) yb[j] = transpose_bytes(xb[j], lane);
+        uint32_t ya[FM], yb[FN];
+        scales(t0, ya, yb);
+        if ((t0 & 4) == 0 && t0 + 8 < steps) issue_scales(t0 + 8, (t0 >> 3 & 1) ^ 1);
         auto step = [&](auto byte, const Fragments& cur, Fragments& next) {
             constexpr int B = decltype(byte)::value;
+            constexpr bool LOAD = B & 1;
             const int t = t0 + B;
             if (t >= steps) return;
-            if constexpr (B & 1) {
-                // the next stage has to be there, and every wave to have read this one
-                stage_barrier<0>();
-                if (t + 3 < steps) issue(t + 3, B >> 1);
-                if constexpr (B == 1) scales(t0 + 4, xa, xb);
+            // the next stage has to be there, and every wave to have read this one
+            if constexpr (LOAD) stage_barrier<0>();
+            // loads to LDS keep their place among its reads, so they are written where they should go
+            constexpr int G = FM + FN, P = FM * FN / G, L = LOADS / G;
+            static_assert(LOADS % G == 0 && FM * FN % G == 0, "an equal share for every read");
+            const uint32_t less = back(t + 3);
+#pragma unroll
+            for (int r = 0; r < G; ++r) {
+                read((B + 1) / 2 % 2, (B + 1) % 2, next, r);      // after the last step: not looked at
+                if constexpr (LOAD) {
+#pragma unroll
+                    for (int i = 0; i < L; ++i) issue(L * r + i, B >> 1, less);
+                }
             }
-            read((B + 1) / 2 % 2, (B + 1) % 2, next);      // after the last step: not looked at
+            if constexpr (LOAD) advance(t + 3);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j) acc[i][j] = mfma_e2m1_at<B>(cur.b[j], cur.a[i], acc[i][j], yb[j], ya[i]);
+            // spread the LDS reads and the loads over the products
 #pragma unroll
-            for (int r = 0; r < FM + FN; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                     // one LDS read
-                __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / (FM + FN), 0);   // its share of products
+            for (int r = 0; r < G; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, P, 0);
+                if constexpr (LOAD) __builtin_amdgcn_sched_group_barrier(0x010, L, 0);
             }
         };
         step(std::integral_constant<int, 0>{}, even, odd);
@@ -324,6 +438,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
         step(std::integral_constant<int, 2>{}, even, odd);
         step(std::integral_constant<int, 3>{}, odd, even);
     }
+    stage_barrier<0>();             // no load to LDS outlives its workgroup
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + wm + 16 * i + li;

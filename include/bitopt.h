@@ -546,7 +546,7 @@ BITOPT_API int bitopt_mx_dequantize(const uint8_t* codes, const uint8_t* scales,
  * instructions.  With an E4M3 operand both are decoded to bf16 (exact while the scaled
  * element is a normal number): the 8-bit matrix instructions align the products of a step
  * to the largest one and drop what lies some 17 bits below it, which an fp32 result shows.
- * k above 2^28 gives UNSUPPORTED.
+ * k above 2^24 gives UNSUPPORTED.
  * Up to 64 rows of a take a form that reads b once and splits k over a workgroup's waves.
  */
 BITOPT_API int bitopt_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_format,
