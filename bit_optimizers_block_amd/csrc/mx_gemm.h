@@ -53,9 +53,15 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     static constexpr int OFFS = along ? N : 1;
     static constexpr int ROWS = NT / PER_ROW;           // memory rows from an item to the next
     static_assert(along || N == 1 || NT % PER_ROW == 0, "items of a thread in one column");
-    uint32_t off[OFFS], soff[codes ? OFFS : 1];
+    // Across, an item's scale byte is loaded with it.  Along, scale bytes go to LDS by direct
+    // loads, eight stages (16 bytes a row) at a time: loaded with the items, a byte each, every
+    // two or four lanes are an access to another row, which cost as much as the codes
+    // themselves.
+    static constexpr bool own_scales = codes && !along;
+    static constexpr int SCALES = codes && along ? R * 16 : 0;
+    uint32_t off[OFFS], soff;
     u32x4 raw[N];
-    uint32_t scale[codes ? N : 1];
+    uint32_t scale[own_scales ? N : 1];
 
     // rows: the operand's rows (columns, if across); r0: the tile's first
     __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int r0, int tid) {
@@ -65,7 +71,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
             const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
             const uint32_t row = along ? (uint32_t)min(a, rows - 1 - r0) : (uint32_t)a;
             off[i] = row * (uint32_t)(codes ? ld : 2 * ld) + (codes ? (four ? b / 2 : b) : 2 * b);
-            if constexpr (codes) soff[i] = row * (uint32_t)ld_sc + b / kMxBlock;
+            if constexpr (own_scales) soff = row * (uint32_t)ld_sc + b / kMxBlock;
         }
     }
     // Whether the stage from k0 lies inside the operand and its offsets fit (wave-uniform).
@@ -86,10 +92,10 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
             if constexpr (codes) raw[i] = *gbl(reinterpret_cast<const u32x4*>(q));
             else raw[i] = ld16_a2(q);
         }
-        if constexpr (codes) {
+        if constexpr (own_scales) {
             const uint8_t* s = sc + row * ld_sc + col / kMxBlock;
 #pragma unroll
-            for (int i = 0; i < N; ++i) scale[i] = gbl(s + (along ? 0 : i * ROWS * ld_sc))[soff[along ? i : 0]];
+            for (int i = 0; i < N; ++i) scale[i] = gbl(s + i * ROWS * ld_sc)[soff];
         }
     }
     __device__ __forceinline__ void load_any(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int rows,
@@ -99,7 +105,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
             const int idx = i * NT + tid;
             const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
             raw[i] = u32x4{0u, 0u, 0u, 0u};
-            if constexpr (codes) scale[i] = 0u;
+            if constexpr (own_scales) scale[i] = 0u;
             if (ITEMS % NT != 0 && idx >= ITEMS) continue;
             // memory row and first element of the item
             const int64_t row = along ? min(r0 + a, rows - 1) : k0 + a;
@@ -115,7 +121,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
                 if (col < width && (along || row < K)) {
                     raw[i] = *gbl(reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(base) + row * ld +
                                                                 (four ? col / 2 : col)));
-                    scale[i] = gbl(sc)[row * ld_sc + col / kMxBlock];
+                    if constexpr (own_scales) scale[i] = gbl(sc)[row * ld_sc + col / kMxBlock];
                 }
             }
         }
@@ -126,16 +132,36 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
         else load_any(base, ld, sc, ld_sc, rows, K, r0, k0, tid);
     }
 
-    // Write p of this thread: eight elements, decoded on the way.
-    __device__ __forceinline__ void store(char* lds, int tid, int p) const {
+    // Scale bytes of the eight stages of group n: rows beyond the last repeat it, bytes beyond
+    // a row's are not looked at.
+    static __device__ __forceinline__ void issue_scales(char* lds, const uint8_t* sc, int64_t ld_sc, int rows, int r0,
+                                                        int n, int tid, int wave) {
+#pragma unroll
+        for (int i = 0; i < R * 4 / NT; ++i) {
+            const int d = i * NT + tid;
+            const uint8_t* p = sc + (int64_t)min(r0 + (d >> 2), rows - 1) * ld_sc +
+                               min((int64_t)n * 16 + (d & 3) * 4, ld_sc - 4);
+            __builtin_amdgcn_global_load_lds((const BITOPT_GLOBAL void*)p,
+                                             (__attribute__((address_space(3))) void*)(lds + i * NT * 4 + wave * 256), 4,
+                                             0, 0);
+        }
+    }
+
+    // Write p of this thread for stage s: eight elements, decoded on the way.
+    __device__ __forceinline__ void store(char* lds, const char* scales, int tid, int s, int p) const {
         const int i = p / (EL / 8), h = p % (EL / 8);
         const int idx = i * NT + tid;
         const int a = idx / PER_ROW, c = idx % PER_ROW * (EL / 8) + h;      // row, 16-byte chunk of it
         if (ITEMS % NT != 0 && idx >= ITEMS) return;
         u32x4 v;
         if constexpr (!codes) v = raw[i];
-        else if constexpr (four) v = mx_half8_e2m1<DT>(raw[i][h], mx_scale_f32(scale[i]));
-        else v = mx_half8_e4m3<DT>(raw[i][2 * h], raw[i][2 * h + 1], mx_scale_f32(scale[i]));
+        else {
+            uint32_t b;
+            if constexpr (own_scales) b = scale[i];
+            else b = *reinterpret_cast<const uint8_t*>(scales + a * 16 + (s & 7) * 2 + c * 8 / kMxBlock);
+            if constexpr (four) v = mx_half8_e2m1<DT>(raw[i][h], mx_scale_f32(b));
+            else v = mx_half8_e4m3<DT>(raw[i][2 * h], raw[i][2 * h + 1], mx_scale_f32(b));
+        }
         const int at = a * PITCH + ((along ? c ^ (a & 7) : c) << 4);
         *reinterpret_cast<u32x4*>(lds + at) = v;
     }
@@ -160,6 +186,15 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     }
 };
 
+// Waits until at most N of the wave's global loads are outstanding and its LDS reads are
+// done, then for the workgroup.  The empty statements keep memory accesses on their side.
+template <int N> __device__ __forceinline__ void stage_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // Waits for the wave's LDS accesses, then for the workgroup; global loads stay in flight.
 // The empty statements keep memory accesses on their side.
 __device__ __forceinline__ void lds_barrier() {
@@ -179,8 +214,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
     using SA = MxStage<DT, ASRC, BM, NT>;
     using SB = MxStage<DT, BSRC, BN, NT>;
-    constexpr int STAGE = SA::BYTES + SB::BYTES;
-    __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
+    constexpr int STAGE = SA::BYTES + SB::BYTES, SCALES = SA::SCALES + SB::SCALES;
+    __shared__ __attribute__((aligned(16))) char lds[2 * STAGE + 2 * SCALES];
 
     int tm, tn;
     mx_tile((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn);
@@ -206,9 +241,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
         sb.load(g.b, g.b_row_bytes, g.b_scales, g.b_row_scales, g.N, g.K, n0, s * kGemmK, tid);
     };
     constexpr int P = SA::PIECES + SB::PIECES;
-    auto store = [&](int buffer, int p) {
-        if (p < SA::PIECES) sa.store(lds + buffer * STAGE, tid, p);
-        else sb.store(lds + buffer * STAGE + SA::BYTES, tid, p - SA::PIECES);
+    // scale bytes of stage s lie in the half of group s / 8
+    auto scales_of = [&](int n) { return lds + 2 * STAGE + (n & 1) * SCALES; };
+    auto issue_scales = [&](int n) {
+        if constexpr (SA::SCALES > 0) SA::issue_scales(scales_of(n), g.a_scales, g.a_row_scales, g.M, m0, n, tid, wave);
+        if constexpr (SB::SCALES > 0)
+            SB::issue_scales(scales_of(n) + SA::SCALES, g.b_scales, g.b_row_scales, g.N, n0, n, tid, wave);
+    };
+    auto store = [&](int buffer, int s, int p) {
+        if (p < SA::PIECES) sa.store(lds + buffer * STAGE, scales_of(s >> 3), tid, s, p);
+        else sb.store(lds + buffer * STAGE + SA::BYTES, scales_of(s >> 3) + SA::SCALES, tid, s, p - SA::PIECES);
     };
     struct Fragments {
         u32x4 a[FM], b[FN];
@@ -228,9 +270,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
     };
 
     if (stages > 0) {
+        issue_scales(0);
         load(0);
+        stage_barrier<0>();
 #pragma unroll
-        for (int p = 0; p < P; ++p) store(0, p);
+        for (int p = 0; p < P; ++p) store(0, 0, p);
         load(1);
         lds_barrier();
     }
@@ -239,6 +283,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
             constexpr int B = decltype(buffer)::value;
             const int s = s0 + B;
             if (s >= stages) return;
+            if constexpr (B == 0 && SCALES > 0) {
+                // The other half was last read for stage s - 1.  Loads complete in order: a wave
+                // that has the items it asks for below has written its part, and the barriers
+                // of the stages until the group begins tell the others.
+                if ((s & 7) == 0 && s + 8 < stages) {
+                    issue_scales((s >> 3) + 1);
+                    asm volatile("" ::: "memory");
+                }
+            }
             Fragments f;
 #pragma unroll
             for (int r = 0; r < G; ++r) read(B, 0, f, r);
@@ -248,7 +301,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
             for (int r = 0; r < G; ++r) {
                 read(B, 1, h, r);
 #pragma unroll
-                for (int p = r * P / G; p < (r + 1) * P / G; ++p) store(B ^ 1, p);
+                for (int p = r * P / G; p < (r + 1) * P / G; ++p) store(B ^ 1, s + 1, p);
             }
             multiply(h);
             load(s + 2);
@@ -285,15 +338,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // accesses: 8192 x 8192 x 8192 took 347 us.)
 
 constexpr int kGemm4K = 128;
-
-// Waits until at most N of the wave's global loads are outstanding and its LDS reads are
-// done, then for the workgroup.  The empty statements keep memory accesses on their side.
-template <int N> __device__ __forceinline__ void stage_barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmArgs g) {
