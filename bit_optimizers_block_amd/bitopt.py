@@ -603,19 +603,25 @@ def _rows(t, name, device=None):
     return rows, cols, cols
 
 
+def _mx_bytes(t, rows, width, name, cols, fmt, device):
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"{name}: expected torch.uint8, got {t.dtype}")
+    if t.shape != (rows, width) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous matrix of {width} bytes a row for {cols} {fmt} columns and as "
+                         f"many rows of codes as of scales, got shape {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on {device}" if device.type == "cuda" else f"{name} must be a device tensor")
+
+
 def _mx_operand(codes, scales, cols, fmt, name, device):
     """Checks an MX matrix of `cols` columns; returns its format and rows."""
-    f = _mx_format(fmt)
+    f = MX_FORMATS.get(fmt)
+    if f is None:
+        _mx_format(fmt)
     pads = (cols + 127) // 128
     rows = codes.size(0) if codes.dim() == 2 else -1
-    for t, what, width in ((codes, "codes", pads * (128 if f else 64)), (scales, "scales", pads * 4)):
-        if t.dtype is not torch.uint8:
-            raise TypeError(f"{name} {what}: expected torch.uint8, got {t.dtype}")
-        if tuple(t.shape) != (rows, width) or not t.is_contiguous():
-            raise ValueError(f"{name} {what}: expected a contiguous matrix of {width} bytes a row for {cols} {fmt} "
-                             f"columns and as many rows of codes as of scales, got shape {tuple(t.shape)}")
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"{name} {what} must be on {device}")
+    _mx_bytes(codes, rows, pads * (128 if f else 64), name + " codes", cols, fmt, device)
+    _mx_bytes(scales, rows, pads * 4, name + " scales", cols, fmt, device)
     return f, rows
 
 
@@ -624,7 +630,7 @@ def _elsewhere(device, stream):
     Otherwise a context that makes `device` (and `stream`, if given) current: results allocated
     inside then belong to the stream that writes them."""
     if stream is None:
-        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the arguments on {device}")
     return torch.cuda.stream(stream)
@@ -639,8 +645,8 @@ def _mx_result(out, rows, cols, dtype, device, name):
     if out is None:
         if dtype not in DTYPES:
             raise TypeError(f"unsupported dtype {dtype}")
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    if tuple(out.shape) != (rows, cols):
+        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device), cols
+    if out.shape != (rows, cols):
         raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(out.shape)}")
     return out, _rows(out, name, device)[2]
 
@@ -649,9 +655,10 @@ def _mx_new(codes, scales, rows, cols, fmt, device, name):
     """Result codes and scales: allocated, or the caller's, checked."""
     f, pads = _mx_format(fmt), (cols + 127) // 128
     if codes is None:
-        codes = torch.empty((rows, pads * (128 if f else 64)), dtype=torch.uint8, device=device)
+        width = pads * (128 if f else 64)
+        codes = torch.empty_strided((rows, width), (width, 1), dtype=torch.uint8, device=device)
         if scales is None:
-            return codes, torch.empty((rows, pads * 4), dtype=torch.uint8, device=device), f
+            return codes, torch.empty_strided((rows, pads * 4), (pads * 4, 1), dtype=torch.uint8, device=device), f
     if scales is None:
         scales = torch.empty((rows, pads * 4), dtype=torch.uint8, device=device)
     if _mx_operand(codes, scales, cols, fmt, name, device)[1] != rows:

@@ -66,18 +66,32 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // 16 bytes at any address aligned to the element: one load or store (the hardware takes
-// unaligned global accesses).
-__device__ __forceinline__ u32x4 ld16_a2(const void* p) {
-    const u32x4a2 v = *(const BITOPT_GLOBAL u32x4a2*)p;
+// unaligned global accesses).  NT: with the non-temporal hint.
+template <bool NT = false> __device__ __forceinline__ u32x4 ld16_a2(const void* p) {
+    const BITOPT_GLOBAL u32x4a2* q = (const BITOPT_GLOBAL u32x4a2*)p;
+    u32x4a2 v;
+    if constexpr (NT) v = __builtin_nontemporal_load(q);
+    else v = *q;
     return u32x4{v.x, v.y, v.z, v.w};
 }
-__device__ __forceinline__ void st16_a2(void* p, u32x4 v) { *(BITOPT_GLOBAL u32x4a2*)p = u32x4a2{v.x, v.y, v.z, v.w}; }
+template <bool NT = false> __device__ __forceinline__ void st16_a2(void* p, u32x4 v) {
+    const u32x4a2 w = {v.x, v.y, v.z, v.w};
+    if constexpr (NT) __builtin_nontemporal_store(w, (BITOPT_GLOBAL u32x4a2*)p);
+    else *(BITOPT_GLOBAL u32x4a2*)p = w;
+}
 __device__ __forceinline__ void st8_a2(void* p, u32x2 v) { *(BITOPT_GLOBAL u32x2a2*)p = u32x2a2{v.x, v.y}; }
-__device__ __forceinline__ f32x4 ld16_a4(const float* p) {
-    const f32x4a4 v = *(const BITOPT_GLOBAL f32x4a4*)p;
+template <bool NT = false> __device__ __forceinline__ f32x4 ld16_a4(const float* p) {
+    const BITOPT_GLOBAL f32x4a4* q = (const BITOPT_GLOBAL f32x4a4*)p;
+    f32x4a4 v;
+    if constexpr (NT) v = __builtin_nontemporal_load(q);
+    else v = *q;
     return f32x4{v.x, v.y, v.z, v.w};
 }
-__device__ __forceinline__ void st16_a4(float* p, f32x4 v) { *(BITOPT_GLOBAL f32x4a4*)p = f32x4a4{v.x, v.y, v.z, v.w}; }
+template <bool NT = false> __device__ __forceinline__ void st16_a4(float* p, f32x4 v) {
+    const f32x4a4 w = {v.x, v.y, v.z, v.w};
+    if constexpr (NT) __builtin_nontemporal_store(w, (BITOPT_GLOBAL f32x4a4*)p);
+    else *(BITOPT_GLOBAL f32x4a4*)p = w;
+}
 
 // The fp32 operand of the scaled conversions for scale byte s: they read its exponent
 // field as an E8M0 byte (0 -> 2^-127, 255 -> NaN).
@@ -98,29 +112,23 @@ template <int FMT> __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t am
 // 2^-e for scale byte e + 127 <= 253: exact, and always a normal number.
 __device__ __forceinline__ float mx_inverse_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
-// Eight scaled values -> codes (nearest, ties to even; -0 keeps its sign).
-__device__ __forceinline__ uint32_t mx_encode8_e2m1(const float v[8]) {
+// Four scaled values -> codes (nearest, ties to even; -0 keeps its sign).
+__device__ __forceinline__ uint32_t mx_encode4_e2m1(const float v[4]) {
     uint32_t r = 0;
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], 1.0f, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], 1.0f, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], 1.0f, 2);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], 1.0f, 3);
-    return r;
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], 1.0f, 1);
 }
-__device__ __forceinline__ uint32_t mx_encode4_e4m3(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t mx_encode4_e4m3(const float v[4]) {
     int r = 0;
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
-    return (uint32_t)r;
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], r, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 }
 
-// Codes -> fp32 (exact; a product below fp32's subnormals cannot arise: 2^-9 * 2^-127).
-__device__ __forceinline__ void mx_decode8_e2m1(uint32_t c, float s, float v[8]) {
+// Four codes -> fp32 (exact: the smallest product, 2^-9 * 2^-127, is an fp32 subnormal).
+__device__ __forceinline__ void mx_decode4_e2m1(uint32_t c, float s, float v[4]) {
     f32x2 p;
     p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0); v[0] = p.x; v[1] = p.y;
     p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1); v[2] = p.x; v[3] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2); v[4] = p.x; v[5] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3); v[6] = p.x; v[7] = p.y;
 }
 __device__ __forceinline__ void mx_decode4_e4m3(uint32_t c, float s, float v[4]) {
     f32x2 p;
@@ -162,8 +170,8 @@ template <int DT> __device__ __forceinline__ u32x4 mx_half8_e4m3(uint32_t c0, ui
 }
 
 // Eight 16-bit elements from any 2-byte-aligned address; the first `n` of them, the rest zero, when n < 8.
-__device__ __forceinline__ u32x4 ld_half8(const uint16_t* p, int n) {
-    if (n >= 8) return ld16_a2(p);
+template <bool NT = false> __device__ __forceinline__ u32x4 ld_half8(const uint16_t* p, int n) {
+    if (n >= 8) return ld16_a2<NT>(p);
     u32x4 r = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j)

@@ -1,9 +1,15 @@
 // MX codec and SwiGLU with its inputs kept in MX E4M3.
 //
 // Every kernel here reads and writes each element once and is bound by HBM.  A lane takes
-// eight consecutive elements of a row (a 16-byte load of 16-bit values), four lanes make
-// a block of 32, and the block maximum meets in two DPP exchanges, so codes leave the
-// registers without LDS or a second pass.
+// 16 bytes of a row (four fp32 or eight 16-bit elements), so a wave's loads and stores are
+// whole lines; eight or four lanes make a block of 32, and the block maximum meets in DPP
+// exchanges, so codes leave the registers without LDS or a second pass.
+//
+// Hints, us at 8192 x 8192 bf16 and 16384 x 8192 bf16: SwiGLU's tensors are past every cache,
+// and streaming them takes the forward pass from 98 to 85 and the backward pass from 99 to
+// 84.  dequantize streams its result (E2M1 68 -> 52).  quantize reads what was just computed:
+// its loads keep the caches (streaming: 60 -> 58 from HBM, but 8.3 -> 9.2 where 8192 x 2048
+// still lies in the Infinity Cache), and so do codes, which the next call reads.
 #include <algorithm>
 
 #include "launch.h"
@@ -19,9 +25,9 @@ struct RowGrid {
 
 constexpr int kRowSteps = 4;
 
-static RowGrid row_grid(int64_t rows, int64_t cols, dim3& grid) {
+static RowGrid row_grid(int64_t rows, int64_t cols, int per_lane, dim3& grid) {
     RowGrid g{};
-    const int64_t items = mx_padded(cols) / 8;
+    const int64_t items = mx_padded(cols) / per_lane;
     g.lanes_log2 = 4;
     while (g.lanes_log2 < 8 && (int64_t{1} << g.lanes_log2) < items) ++g.lanes_log2;
     g.chunks = (int32_t)((items + (int64_t{1} << g.lanes_log2) - 1) >> g.lanes_log2);
@@ -32,35 +38,36 @@ static RowGrid row_grid(int64_t rows, int64_t cols, dim3& grid) {
     return g;
 }
 
-// Eight elements of a row as fp32, from any address aligned to the element; zeros from
-// element n on.
-template <int DT> __device__ __forceinline__ void ld8(const void* base, int64_t e, int n, float v[8]) {
+// Elements per lane.
+template <int DT> constexpr int kPer = DT == kF32 ? 4 : 8;
+
+// One item of a row as fp32, from any address aligned to the element; zeros from element n on.
+template <int DT, bool NT> __device__ __forceinline__ void ld_item(const void* base, int64_t e, int n, float v[kPer<DT>]) {
     if constexpr (DT == kF32) {
         const float* p = reinterpret_cast<const float*>(base) + e;
-        if (n >= 8) {
-            const f32x4 a = ld16_a4(p), b = ld16_a4(p + 4);
+        if (n >= 4) {
+            const f32x4 a = ld16_a4<NT>(p);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+            for (int j = 0; j < 4; ++j) v[j] = a[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = j < n ? gbl(p)[j] : 0.0f;
+            for (int j = 0; j < 4; ++j) v[j] = j < n ? gbl(p)[j] : 0.0f;
         }
     } else {
-        const u32x4 r = ld_half8(reinterpret_cast<const uint16_t*>(base) + e, n);
+        const u32x4 r = ld_half8<NT>(reinterpret_cast<const uint16_t*>(base) + e, n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = widen<DT>(r[j / 2] >> (16 * (j & 1)));
     }
 }
 
-template <int DT> __device__ __forceinline__ void st8(void* base, int64_t e, int n, const float v[8]) {
+template <int DT> __device__ __forceinline__ void st_item(void* base, int64_t e, int n, const float v[kPer<DT>]) {
     if constexpr (DT == kF32) {
         float* p = reinterpret_cast<float*>(base) + e;
-        if (n >= 8) {
-            st16_a4(p, f32x4{v[0], v[1], v[2], v[3]});
-            st16_a4(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+        if (n >= 4) {
+            st16_a4<true>(p, f32x4{v[0], v[1], v[2], v[3]});
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
                 if (j < n) gbl(p)[j] = v[j];
         }
     } else {
@@ -68,7 +75,7 @@ template <int DT> __device__ __forceinline__ void st8(void* base, int64_t e, int
         const u32x4 r = {narrow2<DT>(v[0], v[1]), narrow2<DT>(v[2], v[3]), narrow2<DT>(v[4], v[5]),
                          narrow2<DT>(v[6], v[7])};
         if (n >= 8) {
-            st16_a2(p, r);
+            st16_a2<true>(p, r);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -77,55 +84,66 @@ template <int DT> __device__ __forceinline__ void st8(void* base, int64_t e, int
     }
 }
 
-// Codes of the eight elements of this lane and the scale byte of its block; the block's
-// other elements are in the neighbouring lanes of the aligned group of four.
-template <int FMT>
-__device__ __forceinline__ void encode8(const float x[8], uint32_t c[FMT == kMxE2M1 ? 1 : 2], uint32_t& scale) {
+// Codes of this lane's item: bytes per item, and the type that holds them.
+template <int DT, int FMT> constexpr int kCodeBytes = FMT == kMxE2M1 ? kPer<DT> / 2 : kPer<DT>;
+template <int BYTES> struct CodeWord;
+template <> struct CodeWord<2> { using T = uint16_t; };
+template <> struct CodeWord<4> { using T = uint32_t; };
+template <> struct CodeWord<8> { using T = u32x2; };
+
+// Codes of this lane's item and the scale byte of its block; the block's other elements are
+// in the neighbouring lanes of the aligned group of 32 / kPer.
+template <int DT, int FMT> __device__ __forceinline__ void encode(const float x[kPer<DT>], uint32_t c[2], uint32_t& scale) {
     // the maximum on bit patterns: |NaN| > infinity > every finite value
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+    for (int j = 0; j < kPer<DT>; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));   // quad_perm 1,0,3,2
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));   // quad_perm 2,3,0,1
+    if constexpr (kPer<DT> == 4)
+        m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));   // row_half_mirror
     scale = mx_scale_byte<FMT>(m);
     const bool bad = scale == 255u;
     const float inv = mx_inverse_scale(bad ? 127u : scale);
-    float v[8];
+    float v[kPer<DT>];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = x[j] * inv;
-    if constexpr (FMT == kMxE2M1) {
-        c[0] = bad ? 0u : mx_encode8_e2m1(v);
-    } else {
-        c[0] = bad ? 0u : mx_encode4_e4m3(v[0], v[1], v[2], v[3]);
-        c[1] = bad ? 0u : mx_encode4_e4m3(v[4], v[5], v[6], v[7]);
+    for (int j = 0; j < kPer<DT>; ++j) v[j] = x[j] * inv;
+#pragma unroll
+    for (int h = 0; h < kPer<DT> / 4; ++h) {
+        const uint32_t w = FMT == kMxE2M1 ? mx_encode4_e2m1(v + 4 * h) : mx_encode4_e4m3(v + 4 * h);
+        c[h] = bad ? 0u : w;
     }
 }
 
-template <int FMT>
+template <int DT, int FMT>
 __device__ __forceinline__ void st_codes(uint8_t* codes, uint8_t* scales, int64_t row, int64_t padded, int32_t item,
-                                         const uint32_t c[FMT == kMxE2M1 ? 1 : 2], uint32_t scale) {
-    if constexpr (FMT == kMxE2M1)
-        gbl(reinterpret_cast<uint32_t*>(codes))[row * (padded / 8) + item] = c[0];
-    else
-        gbl(reinterpret_cast<u32x2*>(codes))[row * (padded / 8) + item] = u32x2{c[0], c[1]};
-    if ((item & 3) == 0) gbl(scales)[row * (padded / kMxBlock) + item / 4] = (uint8_t)scale;
+                                         const uint32_t c[2], uint32_t scale) {
+    constexpr int B = kCodeBytes<DT, FMT>, LANES = kMxBlock / kPer<DT>;
+    using T = typename CodeWord<B>::T;
+    T w;
+    if constexpr (B == 8) w = u32x2{c[0], c[1]};
+    else if constexpr (FMT == kMxE2M1 && B == 4) w = c[0] | c[1] << 16;
+    else w = (T)c[0];
+    gbl(reinterpret_cast<T*>(codes))[row * (padded / kPer<DT>) + item] = w;
+    if (item % LANES == 0) gbl(scales)[row * (padded / kMxBlock) + item / LANES] = (uint8_t)scale;
 }
 
-template <int FMT>
+template <int DT, int FMT>
 __device__ __forceinline__ void ld_codes(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t padded,
-                                         int32_t item, float v[8]) {
-    const float s = mx_scale_f32(gbl(scales)[row * (padded / kMxBlock) + item / 4]);
-    if constexpr (FMT == kMxE2M1) {
-        mx_decode8_e2m1(gbl(reinterpret_cast<const uint32_t*>(codes))[row * (padded / 8) + item], s, v);
-    } else {
-        const u32x2 c = gbl(reinterpret_cast<const u32x2*>(codes))[row * (padded / 8) + item];
-        mx_decode4_e4m3(c.x, s, v);
-        mx_decode4_e4m3(c.y, s, v + 4);
+                                         int32_t item, float v[kPer<DT>]) {
+    using T = typename CodeWord<kCodeBytes<DT, FMT>>::T;
+    const float s = mx_scale_f32(gbl(scales)[row * (padded / kMxBlock) + item / (kMxBlock / kPer<DT>)]);
+    const T w = gbl(reinterpret_cast<const T*>(codes))[row * (padded / kPer<DT>) + item];
+#pragma unroll
+    for (int h = 0; h < kPer<DT> / 4; ++h) {
+        if constexpr (FMT == kMxE2M1) mx_decode4_e2m1((uint32_t)w >> (16 * h), s, v + 4 * h);
+        else if constexpr (kPer<DT> == 4) mx_decode4_e4m3((uint32_t)w, s, v);
+        else mx_decode4_e4m3(w[h], s, v + 4 * h);
     }
 }
 
-// Runs f(row, item) for every eight-element item of the padded rows.  All four lanes of a
-// block are in or out together (items per row is a multiple of 16).
+// Runs f(row, item) for every item of the padded rows.  The lanes of a block are in or out
+// together (items per row is a multiple of 16).
 template <class F> __device__ __forceinline__ void for_items(const RowGrid& g, int64_t rows, int32_t items, F f) {
     const int lanes = 1 << g.lanes_log2;
     const int32_t item = (int32_t)blockIdx.x * lanes + ((int)threadIdx.x & (lanes - 1));
@@ -140,27 +158,27 @@ template <class F> __device__ __forceinline__ void for_items(const RowGrid& g, i
     for (; row < rows; row += stride) f(row, item);
 }
 
-__device__ __forceinline__ int item_elems(int64_t cols, int32_t item) {
-    return (int)max((int64_t)0, min((int64_t)8, cols - 8 * (int64_t)item));
+template <int DT> __device__ __forceinline__ int item_elems(int64_t cols, int32_t item) {
+    return (int)max((int64_t)0, min((int64_t)kPer<DT>, cols - kPer<DT> * (int64_t)item));
 }
 
 template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_mx_quantize(MxCodecArgs a, RowGrid g) {
     const int64_t padded = mx_padded(a.cols);
-    for_items(g, a.rows, (int32_t)(padded / 8), [&](int64_t row, int32_t item) {
-        float v[8];
+    for_items(g, a.rows, (int32_t)(padded / kPer<DT>), [&](int64_t row, int32_t item) {
+        float v[kPer<DT>];
         uint32_t c[2], s;
-        ld8<DT>(a.x, row * a.ldx + 8 * (int64_t)item, item_elems(a.cols, item), v);
-        encode8<FMT>(v, c, s);
-        st_codes<FMT>(a.codes, a.scales, row, padded, item, c, s);
+        ld_item<DT, false>(a.x, row * a.ldx + kPer<DT> * (int64_t)item, item_elems<DT>(a.cols, item), v);
+        encode<DT, FMT>(v, c, s);
+        st_codes<DT, FMT>(a.codes, a.scales, row, padded, item, c, s);
     });
 }
 
 template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_mx_dequantize(MxCodecArgs a, RowGrid g) {
     const int64_t padded = mx_padded(a.cols);
-    for_items(g, a.rows, (int32_t)(padded / 8), [&](int64_t row, int32_t item) {
-        float v[8];
-        ld_codes<FMT>(a.codes, a.scales, row, padded, item, v);
-        st8<DT>(a.out, row * a.ldo + 8 * (int64_t)item, item_elems(a.cols, item), v);
+    for_items(g, a.rows, (int32_t)(padded / kPer<DT>), [&](int64_t row, int32_t item) {
+        float v[kPer<DT>];
+        ld_codes<DT, FMT>(a.codes, a.scales, row, padded, item, v);
+        st_item<DT>(a.out, row * a.ldo + kPer<DT> * (int64_t)item, item_elems<DT>(a.cols, item), v);
     });
 }
 
@@ -175,41 +193,41 @@ template <int DT> __device__ __forceinline__ float sigmoid(float g) {
 // y = gate * sigmoid(gate) * up, and both inputs in MX E4M3.
 template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_forward(SwigluArgs a, RowGrid g) {
     const int64_t padded = mx_padded(a.cols);
-    for_items(g, a.rows, (int32_t)(padded / 8), [&](int64_t row, int32_t item) {
-        const int n = item_elems(a.cols, item);
-        const int64_t e = 8 * (int64_t)item;
-        float x[8], u[8], y[8];
+    for_items(g, a.rows, (int32_t)(padded / kPer<DT>), [&](int64_t row, int32_t item) {
+        const int n = item_elems<DT>(a.cols, item);
+        const int64_t e = kPer<DT> * (int64_t)item;
+        float x[kPer<DT>], u[kPer<DT>], y[kPer<DT>];
         uint32_t c[2], s;
-        ld8<DT>(a.gate, row * a.ldg + e, n, x);
-        ld8<DT>(a.up, row * a.ldu + e, n, u);
+        ld_item<DT, true>(a.gate, row * a.ldg + e, n, x);
+        ld_item<DT, true>(a.up, row * a.ldu + e, n, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j] * sigmoid<DT>(x[j]) * u[j];
-        st8<DT>(a.y, row * a.ldy + e, n, y);
-        encode8<kMxE4M3>(x, c, s);
-        st_codes<kMxE4M3>(a.gate_codes, a.gate_scales, row, padded, item, c, s);
-        encode8<kMxE4M3>(u, c, s);
-        st_codes<kMxE4M3>(a.up_codes, a.up_scales, row, padded, item, c, s);
+        for (int j = 0; j < kPer<DT>; ++j) y[j] = x[j] * sigmoid<DT>(x[j]) * u[j];
+        st_item<DT>(a.y, row * a.ldy + e, n, y);
+        encode<DT, kMxE4M3>(x, c, s);
+        st_codes<DT, kMxE4M3>(a.gate_codes, a.gate_scales, row, padded, item, c, s);
+        encode<DT, kMxE4M3>(u, c, s);
+        st_codes<DT, kMxE4M3>(a.up_codes, a.up_scales, row, padded, item, c, s);
     });
 }
 
 // With s = sigmoid(g): dgate = dy u (s + g s (1 - s)), dup = dy g s, at the saved values.
 template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_backward(SwigluArgs a, RowGrid g) {
     const int64_t padded = mx_padded(a.cols);
-    for_items(g, a.rows, (int32_t)(padded / 8), [&](int64_t row, int32_t item) {
-        const int n = item_elems(a.cols, item);
-        const int64_t e = 8 * (int64_t)item;
-        float x[8], u[8], d[8], dg[8], du[8];
-        ld8<DT>(a.dy, row * a.ldy + e, n, d);
-        ld_codes<kMxE4M3>(a.gate_codes, a.gate_scales, row, padded, item, x);
-        ld_codes<kMxE4M3>(a.up_codes, a.up_scales, row, padded, item, u);
+    for_items(g, a.rows, (int32_t)(padded / kPer<DT>), [&](int64_t row, int32_t item) {
+        const int n = item_elems<DT>(a.cols, item);
+        const int64_t e = kPer<DT> * (int64_t)item;
+        float x[kPer<DT>], u[kPer<DT>], d[kPer<DT>], dg[kPer<DT>], du[kPer<DT>];
+        ld_item<DT, true>(a.dy, row * a.ldy + e, n, d);
+        ld_codes<DT, kMxE4M3>(a.gate_codes, a.gate_scales, row, padded, item, x);
+        ld_codes<DT, kMxE4M3>(a.up_codes, a.up_scales, row, padded, item, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kPer<DT>; ++j) {
             const float s = sigmoid<DT>(x[j]);
             dg[j] = d[j] * u[j] * s * (1.0f + x[j] * (1.0f - s));
             du[j] = d[j] * x[j] * s;
         }
-        st8<DT>(a.dgate, row * a.lddg + e, n, dg);
-        st8<DT>(a.dup, row * a.lddu + e, n, du);
+        st_item<DT>(a.dgate, row * a.lddg + e, n, dg);
+        st_item<DT>(a.dup, row * a.lddu + e, n, du);
     });
 }
 
@@ -218,7 +236,7 @@ template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_backward(
 #define BITOPT_MX_LAUNCH(kernel, args)                                              \
     do {                                                                            \
         dim3 grid;                                                                  \
-        const RowGrid g = row_grid((args).rows, (args).cols, grid);                 \
+        const RowGrid g = row_grid((args).rows, (args).cols, dtype == kF32 ? 4 : 8, grid);                 \
         hipLaunchKernelGGL(HIP_KERNEL_NAME(kernel), grid, dim3(kThreads), 0, s, args, g); \
         return hipGetLastError();                                                   \
     } while (0)
