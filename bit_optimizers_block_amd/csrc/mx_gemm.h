@@ -37,8 +37,10 @@ constexpr int kGemmK = 64;      // contraction elements per LDS stage of the 16-
 // the segments does the same, but costs a register of addresses for every fragment).
 template <int DT, int SRC, int R, int NT> struct MxStage {
     static constexpr bool along = mx_is_along(SRC), codes = mx_is_codes(SRC), four = mx_is_4bit(SRC);
-    // elements per thread item: one 16-byte load
-    static constexpr int EL = !codes ? 8 : (four ? 32 : 16);
+    // elements per thread item: one 16-byte load, or one of 8 where a small tile's 4-bit codes
+    // would leave half of the workgroup without
+    static constexpr bool HALF = four && R * kGemmK / 32 < NT;
+    static constexpr int EL = !codes ? 8 : (four && !HALF ? 32 : 16);
     static constexpr int PER_ROW = (along ? kGemmK : R) / EL;
     static constexpr int ITEMS = PER_ROW * (along ? R : kGemmK);
     static constexpr int N = (ITEMS + NT - 1) / NT;
@@ -63,6 +65,14 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     u32x4 raw[N];
     uint32_t scale[own_scales ? N : 1];
 
+    static __device__ __forceinline__ u32x4 ld_codes(const uint8_t* p) {
+        if constexpr (HALF) {
+            const u32x2 v = *gbl(reinterpret_cast<const u32x2*>(p));
+            return u32x4{v.x, v.y, 0u, 0u};
+        } else {
+            return *gbl(reinterpret_cast<const u32x4*>(p));
+        }
+    }
     // rows: the operand's rows (columns, if across); r0: the tile's first
     __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int r0, int tid) {
 #pragma unroll
@@ -89,7 +99,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const uint8_t* q = p + i * next + off[along ? i : 0];
-            if constexpr (codes) raw[i] = *gbl(reinterpret_cast<const u32x4*>(q));
+            if constexpr (codes) raw[i] = ld_codes(q);
             else raw[i] = ld16_a2(q);
         }
         if constexpr (own_scales) {
@@ -119,8 +129,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
                 // rows of codes are padded with zeros to 128 elements
                 const int width = (int)mx_padded(along ? K : rows);
                 if (col < width && (along || row < K)) {
-                    raw[i] = *gbl(reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(base) + row * ld +
-                                                                (four ? col / 2 : col)));
+                    raw[i] = ld_codes(reinterpret_cast<const uint8_t*>(base) + row * ld + (four ? col / 2 : col));
                     if constexpr (own_scales) scale[i] = gbl(sc)[row * ld_sc + col / kMxBlock];
                 }
             }
@@ -437,7 +446,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
             for (int i = 0; i < LOADS; ++i) issue(i, s, back(2 * s));
             advance(2 * s);
         }
-        stage_barrier<0>();
+        stage_barrier<LOADS>();         // all but the second stage
 #pragma unroll
         for (int r = 0; r < FM + FN; ++r) read(0, 0, even, r);
     }
@@ -511,7 +520,7 @@ template <int DT, int ASRC, int BSRC> hipError_t mx_gemm16(const MxGemmArgs& g, 
             return hipGetLastError();
         },
         [&](dim3 grid) {
-            hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, 128, 128, 64, 64>), grid, dim3(256), 0, s, g);
+            hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, 128, 128, 64, 32>), grid, dim3(512), 0, s, g);
             return hipGetLastError();
         },
         [&](dim3 grid) {
