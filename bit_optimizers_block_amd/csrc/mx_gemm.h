@@ -213,11 +213,17 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Workgroup tile BM x BN, wave tile WM x WN.  Two LDS buffers of one stage (64 contraction
-// elements, two steps of 32).  While the fragments of a step are multiplied, those of the
-// next are read.  When the second step of a stage begins, all of the stage is in registers:
-// its buffer takes the stage after the next, whose loads were sent two steps before, and the
-// loads of the stage after that are sent.  One barrier per stage.
+// Workgroup tile BM x BN, wave tile WM x WN.  Two LDS buffers of one stage of 64 contraction
+// elements.  While a stage is multiplied, the next one, whose loads were sent a stage before,
+// is decoded and written to the other buffer between the products, and the loads of the one
+// after that are sent; the barrier that ends a stage leaves them in flight.
+//
+// Bound: LDS.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and 32 KB
+// of writes per 32 contraction elements, 1024 cycles at 128 bytes, against 1024 cycles of
+// products; two waves a SIMD fill each other's waits.  Measured at 8192 x 8192 x 2048, bf16:
+// input grad 217 us (1270 TFLOP/s), weight grad 236 us, forward 223 us.  Writing the next
+// stage after the products instead: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic
+// is a quarter less, leave one wave a SIMD and too few registers: 360, 499, 322.
 template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
@@ -345,6 +351,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // and the matrix instruction selects byte t itself.  (Loaded from global memory in that
 // pattern, 64 separate dwords an instruction, scales were two thirds of the cache's
 // accesses: 8192 x 8192 x 8192 took 347 us.)
+//
+// Measured: 8192 x 8192 x 8192 266 us (4130 TFLOP/s; the products alone 239 us at the clock
+// that they leave), 8192 x 8192 x 2048 111 us, of which 50 us are steps: with one workgroup
+// a CU, each of the four rounds of tiles begins with empty buffers and ends in 128 KB of
+// results that nothing overlaps.  Eight waves of 128 x 64 with 32 KB stages took 136 us, going
+// through the tiles in one resident grid with the next one's loads ahead of the last one's
+// stores 154 us (the registers for both spill).
 
 constexpr int kGemm4K = 128;
 
@@ -503,7 +516,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
 // ------------------------------------------------------------------------ tile choice
 
 // Launches `big` (256 x 256 tiles), `mid` (128 x 128) or `small` (64 x 64): the largest
-// tile whose grid still gives the 256 CUs about one workgroup each.
+// tile whose grid still occupies most of the 256 CUs.  Forward product, E2M1, us with big,
+// mid and small tiles at M x N x K (big tiles, mid tiles): 3584 x 3584 x 2048 (196, 784) 57,
+// 72, 88; 4096 x 2048 x 8192 (128, 512) 195, 159, 225; 1792 x 1792 x 2048 (49, 196) 54, 24,
+// 30; 2048 x 1024 x 2048 (32, 128) 52, 23, 19.
 template <class Big, class Mid, class Small>
 hipError_t mx_by_tile(const MxGemmArgs& g, Big big, Mid mid, Small small) {
     auto tiles = [&](int t) { return ((int64_t)g.M + t - 1) / t * (((int64_t)g.N + t - 1) / t); };

@@ -13,9 +13,11 @@
 // four lanes read 64 consecutive bytes.  Codes are loaded 16 bytes a lane as well and
 // brought into that order by exchanges between lane groups (E2M1: a 4 x 4 transpose of
 // dwords, four exchanges for 128 elements; E4M3: half a transpose, four exchanges, which
-// leaves groups 1 and 2 with each other's elements, so the other operand follows).  Loading
-// each lane's 64 bytes of A in place instead touches 64 segments an instruction and took
-// 1.6 to 2 times as long.
+// leaves groups 1 and 2 with each other's elements, so the other operand follows).
+//
+// Measured, bf16 A, E2M1 B: one row against 50257 x 2048 (55 MB of codes and scales) 16.3 us,
+// two E2M1 operands 12.9 us, of which a launch is 2.6; 64 rows against 8192 x 8192 39 us,
+// bound by A's rows, which every workgroup reads from the caches.
 #include <algorithm>
 #include <type_traits>
 
@@ -239,7 +241,8 @@ __global__ __launch_bounds__(WAVES * 64) void k_mx_skinny(MxGemmArgs g) {
 
 // Up to 16 rows of A and a contraction that the waves hold at four chunks each: A's
 // fragments are loaded once and stay in registers, and a workgroup goes through tiles of 16
-// rows of B, the next tile's codes on their way while one is multiplied.
+// rows of B, the next tile's codes on their way while one is multiplied (one row against
+// 50257 x 2048: 16.3 us, against 20.8 with A's rows loaded for every tile).
 template <int DT, int XSRC, int FMT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_mx_tokens(MxGemmArgs g) {
     constexpr bool scaled = XSRC == kXE2M1 && FMT == kMxE2M1;
