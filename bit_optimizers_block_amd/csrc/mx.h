@@ -169,10 +169,27 @@ template <int DT> __device__ __forceinline__ u32x4 mx_half8_e4m3(uint32_t c0, ui
     return r;
 }
 
-// Eight 16-bit elements from any 2-byte-aligned address; the first `n` of them, the rest zero, when n < 8.
-template <bool NT = false> __device__ __forceinline__ u32x4 ld_half8(const uint16_t* p, int n) {
+// Eight 16-bit elements moved d places down (1 <= d <= 7), zeros from above.
+__device__ __forceinline__ u32x4 half_shift(u32x4 r, int d) {
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+        if (d >= 2 * (w + 1)) r = u32x4{r.y, r.z, r.w, 0u};
+    // two places a word above; now half of one
+    if (d & 1)
+        r = u32x4{__builtin_amdgcn_alignbit(r.y, r.x, 16), __builtin_amdgcn_alignbit(r.z, r.y, 16),
+                  __builtin_amdgcn_alignbit(r.w, r.z, 16), r.w >> 16};
+    return r;
+}
+
+// Eight 16-bit elements from any 2-byte-aligned address; the first `n` of them, the rest
+// zero, when n < 8.  Where the row holds eight elements up to there (`before` of them precede
+// p), they are the last of one load that ends with the row; only shorter rows are read
+// element by element, which waits for every element.
+template <bool NT = false> __device__ __forceinline__ u32x4 ld_half8(const uint16_t* p, int n, int64_t before) {
     if (n >= 8) return ld16_a2<NT>(p);
     u32x4 r = {0u, 0u, 0u, 0u};
+    if (n <= 0) return r;
+    if (before + n >= 8) return half_shift(ld16_a2<NT>(p - (8 - n)), 8 - n);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (j < n) r[j / 2] |= (uint32_t)gbl(p)[j] << (16 * (j & 1));

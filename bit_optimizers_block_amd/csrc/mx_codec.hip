@@ -42,7 +42,9 @@ static RowGrid row_grid(int64_t rows, int64_t cols, int per_lane, dim3& grid) {
 template <int DT> constexpr int kPer = DT == kF32 ? 4 : 8;
 
 // One item of a row as fp32, from any address aligned to the element; zeros from element n on.
-template <int DT, bool NT> __device__ __forceinline__ void ld_item(const void* base, int64_t e, int n, float v[kPer<DT>]) {
+// before: elements of the row ahead of it.
+template <int DT, bool NT> __device__ __forceinline__ void ld_item(const void* base, int64_t e, int n, int64_t before,
+                                                                         float v[kPer<DT>]) {
     if constexpr (DT == kF32) {
         const float* p = reinterpret_cast<const float*>(base) + e;
         if (n >= 4) {
@@ -54,7 +56,7 @@ template <int DT, bool NT> __device__ __forceinline__ void ld_item(const void* b
             for (int j = 0; j < 4; ++j) v[j] = j < n ? gbl(p)[j] : 0.0f;
         }
     } else {
-        const u32x4 r = ld_half8<NT>(reinterpret_cast<const uint16_t*>(base) + e, n);
+        const u32x4 r = ld_half8<NT>(reinterpret_cast<const uint16_t*>(base) + e, n, before);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = widen<DT>(r[j / 2] >> (16 * (j & 1)));
     }
@@ -167,7 +169,7 @@ template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_mx_quan
     for_items(g, a.rows, (int32_t)(padded / kPer<DT>), [&](int64_t row, int32_t item) {
         float v[kPer<DT>];
         uint32_t c[2], s;
-        ld_item<DT, false>(a.x, row * a.ldx + kPer<DT> * (int64_t)item, item_elems<DT>(a.cols, item), v);
+        ld_item<DT, false>(a.x, row * a.ldx + kPer<DT> * (int64_t)item, item_elems<DT>(a.cols, item), kPer<DT> * (int64_t)item, v);
         encode<DT, FMT>(v, c, s);
         st_codes<DT, FMT>(a.codes, a.scales, row, padded, item, c, s);
     });
@@ -198,8 +200,8 @@ template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_forward(S
         const int64_t e = kPer<DT> * (int64_t)item;
         float x[kPer<DT>], u[kPer<DT>], y[kPer<DT>];
         uint32_t c[2], s;
-        ld_item<DT, true>(a.gate, row * a.ldg + e, n, x);
-        ld_item<DT, true>(a.up, row * a.ldu + e, n, u);
+        ld_item<DT, true>(a.gate, row * a.ldg + e, n, e, x);
+        ld_item<DT, true>(a.up, row * a.ldu + e, n, e, u);
 #pragma unroll
         for (int j = 0; j < kPer<DT>; ++j) y[j] = x[j] * sigmoid<DT>(x[j]) * u[j];
         st_item<DT>(a.y, row * a.ldy + e, n, y);
@@ -217,7 +219,7 @@ template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_backward(
         const int n = item_elems<DT>(a.cols, item);
         const int64_t e = kPer<DT> * (int64_t)item;
         float x[kPer<DT>], u[kPer<DT>], d[kPer<DT>], dg[kPer<DT>], du[kPer<DT>];
-        ld_item<DT, true>(a.dy, row * a.ldy + e, n, d);
+        ld_item<DT, true>(a.dy, row * a.ldy + e, n, e, d);
         ld_codes<DT, kMxE4M3>(a.gate_codes, a.gate_scales, row, padded, item, x);
         ld_codes<DT, kMxE4M3>(a.up_codes, a.up_scales, row, padded, item, u);
 #pragma unroll

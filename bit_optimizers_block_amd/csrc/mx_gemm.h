@@ -61,6 +61,11 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     // themselves.
     static constexpr bool own_scales = codes && !along;
     static constexpr int SCALES = codes && along ? R * 16 : 0;
+    // Where a 16-bit operand's memory rows end in a stage, an item is one load of the row's last
+    // eight elements at most, and store() shifts it and zeroes what lies beyond (read element
+    // by element, a ragged edge waited for every one: 777 x 1001 x 513 weight gradient 15 us).
+    static constexpr bool SHIFTS = !codes;
+    int span;               // elements of a memory row: all of them (along), from the tile's first (across)
     uint32_t off[OFFS], soff;
     u32x4 raw[N];
     uint32_t scale[own_scales ? N : 1];
@@ -74,11 +79,14 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
         }
     }
     // rows: the operand's rows (columns, if across); r0: the tile's first
-    __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int r0, int tid) {
+    __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int K, int r0, int tid) {
+        span = along ? K : rows - r0;
 #pragma unroll
         for (int i = 0; i < OFFS; ++i) {
             const int idx = min(i * NT + tid, ITEMS - 1);
-            const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
+            const int a = idx / PER_ROW;
+            int b = idx % PER_ROW * EL;
+            if constexpr (SHIFTS && !along) b = max(0, min(b, rows - r0 - 8));
             const uint32_t row = along ? (uint32_t)min(a, rows - 1 - r0) : (uint32_t)a;
             off[i] = row * (uint32_t)(codes ? ld : 2 * ld) + (codes ? (four ? b / 2 : b) : 2 * b);
             if constexpr (own_scales) soff = row * (uint32_t)ld_sc + b / kMxBlock;
@@ -88,7 +96,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     static __device__ __forceinline__ bool inside(int64_t ld, int rows, int K, int r0, int k0) {
         if (ld >= (1 << 22)) return false;
         if (along) return codes || k0 + kGemmK <= K;
-        return k0 + kGemmK <= K && r0 + R <= (codes ? (int)mx_padded(rows) : rows);
+        return k0 + kGemmK <= K && (codes ? r0 + R <= (int)mx_padded(rows) : rows - r0 >= 8);
     }
     __device__ __forceinline__ void load_inside(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int r0,
                                                 int k0) {
@@ -121,10 +129,16 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
             const int64_t row = along ? min(r0 + a, rows - 1) : k0 + a;
             const int col = (along ? k0 : r0) + b;
             if constexpr (!codes) {
+                if (span >= 8) {
+                    if (along || row < K)
+                        raw[i] = ld16_a2(reinterpret_cast<const uint16_t*>(base) + row * ld +
+                                         min(col, (along ? K : rows) - 8));
+                    continue;
+                }
                 // elements left in the row: beyond it, and on rows past the contraction, zero
                 const int left = along ? K - col : (row < K ? rows - col : 0);
                 if (left > 0)
-                    raw[i] = ld_half8(reinterpret_cast<const uint16_t*>(base) + row * ld + col, left);
+                    raw[i] = ld_half8(reinterpret_cast<const uint16_t*>(base) + row * ld + col, left, 0);
             } else {
                 // rows of codes are padded with zeros to 128 elements
                 const int width = (int)mx_padded(along ? K : rows);
@@ -163,8 +177,14 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
         const int a = idx / PER_ROW, c = idx % PER_ROW * (EL / 8) + h;      // row, 16-byte chunk of it
         if (ITEMS % NT != 0 && idx >= ITEMS) return;
         u32x4 v;
-        if constexpr (!codes) v = raw[i];
-        else {
+        if constexpr (!codes) {
+            v = raw[i];
+            const int end = along ? span - s * kGemmK : span;
+            if (span >= 8 && end < (along ? kGemmK : R)) {
+                const int left = end - c * 8;
+                v = left >= 8 ? v : left > 0 ? half_shift(v, 8 - left) : u32x4{0u, 0u, 0u, 0u};
+            }
+        } else {
             uint32_t b;
             if constexpr (own_scales) b = scale[i];
             else b = *reinterpret_cast<const uint8_t*>(scales + a * 16 + (s & 7) * 2 + c * 8 / kMxBlock);
@@ -242,8 +262,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 
     SA sa;
     SB sb;
-    sa.init(lda, g.a_row_scales, g.M, m0, tid);
-    sb.init(g.b_row_bytes, g.b_row_scales, g.N, n0, tid);
+    sa.init(lda, g.a_row_scales, g.M, g.K, m0, tid);
+    sb.init(g.b_row_bytes, g.b_row_scales, g.N, g.K, n0, tid);
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -336,14 +356,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // ------------------------------------------------------------------ both operands E2M1
 
 // Codes go from global memory straight to LDS in two stages of 256 contraction elements in
-// turn: 128 bytes of codes a row, a whole cache line (stages of 64 bytes a row fetched
-// lines twice).  A stage is multiplied in two steps of 128.  While the fragments of one step
-// are multiplied, those of the next are read from LDS; when the second step of a stage
-// begins, all of the stage is in registers and the stage after the next is asked for into
-// its buffer, two steps before it is needed.  That is one barrier per stage.  A wave's load
-// fills 1024 consecutive bytes of LDS, so the swizzle that spreads a fragment's rows over
-// the banks -- 16-byte chunk c of row r lies at chunk c ^ (r % 8) -- is applied to the source
-// address.
+// turn: 128 bytes of codes a row, a whole cache line.  A stage is multiplied in two steps of
+// 128.  Once the second step's fragments are in registers, and the barrier has said so for
+// every wave and that the next stage is there, the stage after it is asked for into the
+// buffer, under the products.  That is one barrier per stage.  A wave's load fills 1024
+// consecutive bytes of LDS, so the swizzle that spreads a fragment's rows over the banks --
+// 16-byte chunk c of row r lies at chunk c ^ (r % 8) -- is applied to the source address.
 //
 // Scales come by the same direct loads, eight steps (32 bytes a row) at a time.  Lane (row
 // i, group q) reads the four scale bytes of its row in step q of four; a byte transpose
@@ -352,12 +370,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // pattern, 64 separate dwords an instruction, scales were two thirds of the cache's
 // accesses: 8192 x 8192 x 8192 took 347 us.)
 //
-// Measured: 8192 x 8192 x 8192 266 us (4130 TFLOP/s; the products alone 239 us at the clock
-// that they leave), 8192 x 8192 x 2048 111 us, of which 50 us are steps: with one workgroup
-// a CU, each of the four rounds of tiles begins with empty buffers and ends in 128 KB of
-// results that nothing overlaps.  Eight waves of 128 x 64 with 32 KB stages took 136 us, going
-// through the tiles in one resident grid with the next one's loads ahead of the last one's
-// stores 154 us (the registers for both spill).
+// Measured: 8192 x 8192 x 8192 264 us (4170 TFLOP/s), 8192 x 8192 x 2048 100 us, of which the
+// steps are 55: with one workgroup a CU, each of the four rounds of tiles begins with empty
+// buffers and ends in 128 KB of results that nothing overlaps.  Four waves of 128 x 128 that
+// read a step's fragments under the one before took 266 and 110 us; eight such waves spill.
+// One resident grid with the next tile's loads ahead of the last one's stores took 154 us at
+// the second size, non-temporal stores 138 (against 116 at the time).
 
 constexpr int kGemm4K = 128;
 
@@ -450,7 +468,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
         else f.a[r - FN] = *reinterpret_cast<const u32x4*>(cur + (wm + 16 * (r - FN)) * 128);
     };
 
-    Fragments even, odd;
     if (steps > 0) {
         issue_scales(0, 0);
 #pragma unroll
@@ -458,51 +475,38 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) issue(i, s, back(2 * s));
             advance(2 * s);
+            asm volatile("" ::: "memory");      // in this order: the wait below counts on it
         }
         stage_barrier<LOADS>();         // all but the second stage
-#pragma unroll
-        for (int r = 0; r < FM + FN; ++r) read(0, 0, even, r);
     }
     for (int t0 = 0; t0 < steps; t0 += 4) {
         uint32_t ya[FM], yb[FN];
         scales(t0, ya, yb);
         if ((t0 & 4) == 0 && t0 + 8 < steps) issue_scales(t0 + 8, (t0 >> 3 & 1) ^ 1);
-        auto step = [&](auto byte, const Fragments& cur, Fragments& next) {
+        auto step = [&](auto byte) {
             constexpr int B = decltype(byte)::value;
-            constexpr bool LOAD = B & 1;
             const int t = t0 + B;
             if (t >= steps) return;
-            // the next stage has to be there, and every wave to have read this one
-            if constexpr (LOAD) stage_barrier<0>();
-            // loads to LDS keep their place among its reads, so they are written where they should go
-            constexpr int G = FM + FN, P = FM * FN / G, L = LOADS / G;
-            static_assert(LOADS % G == 0 && FM * FN % G == 0, "an equal share for every read");
-            const uint32_t less = back(t + 3);
+            Fragments f;
 #pragma unroll
-            for (int r = 0; r < G; ++r) {
-                read((B + 1) / 2 % 2, (B + 1) % 2, next, r);      // after the last step: not looked at
-                if constexpr (LOAD) {
+            for (int r = 0; r < FM + FN; ++r) read(B / 2, B % 2, f, r);
+            if constexpr (B & 1) {
+                // the next stage has to be there, and every wave to have read this one
+                stage_barrier<0>();
+                const uint32_t less = back(t + 3);
 #pragma unroll
-                    for (int i = 0; i < L; ++i) issue(L * r + i, B >> 1, less);
-                }
+                for (int i = 0; i < LOADS; ++i) issue(i, B >> 1, less);
+                advance(t + 3);
             }
-            if constexpr (LOAD) advance(t + 3);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma_e2m1_at<B>(cur.b[j], cur.a[i], acc[i][j], yb[j], ya[i]);
-            // spread the LDS reads and the loads over the products
-#pragma unroll
-            for (int r = 0; r < G; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, P, 0);
-                if constexpr (LOAD) __builtin_amdgcn_sched_group_barrier(0x010, L, 0);
-            }
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma_e2m1_at<B>(f.b[j], f.a[i], acc[i][j], yb[j], ya[i]);
         };
-        step(std::integral_constant<int, 0>{}, even, odd);
-        step(std::integral_constant<int, 1>{}, odd, even);
-        step(std::integral_constant<int, 2>{}, even, odd);
-        step(std::integral_constant<int, 3>{}, odd, even);
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 3>{});
     }
     stage_barrier<0>();             // no load to LDS outlives its workgroup
 #pragma unroll

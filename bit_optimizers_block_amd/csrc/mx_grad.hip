@@ -16,11 +16,11 @@ hipError_t launch_mx_matmul(const MxGemmArgs& g, int a_fmt, int b_fmt, hipStream
         return mx_by_tile(
             g,
             [&](dim3 grid) {
-                hipLaunchKernelGGL((k_mx_gemm4<256, 256, 128, 128>), grid, dim3(256), 0, s, g);
+                hipLaunchKernelGGL((k_mx_gemm4<256, 256, 128, 64>), grid, dim3(512), 0, s, g);
                 return hipGetLastError();
             },
             [&](dim3 grid) {
-                hipLaunchKernelGGL((k_mx_gemm4<128, 128, 64, 64>), grid, dim3(256), 0, s, g);
+                hipLaunchKernelGGL((k_mx_gemm4<128, 128, 64, 32>), grid, dim3(512), 0, s, g);
                 return hipGetLastError();
             },
             [&](dim3 grid) {

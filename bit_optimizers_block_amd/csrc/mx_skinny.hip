@@ -101,7 +101,7 @@ __device__ __forceinline__ void ld_chunk16(const uint16_t* row, int chunk, int o
             for (int j = 0; j < 4; ++j) f[j] = ld16_a2(row + k + 32 * j);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = ld_half8(row + k + 32 * j, K - k - 32 * j);
+            for (int j = 0; j < 4; ++j) f[j] = ld_half8(row + k + 32 * j, K - k - 32 * j, k + 32 * j);
         }
     }
 }

@@ -157,9 +157,13 @@ def test_dequantize_every_code_and_scale(dtype, fmt):
 
 # ------------------------------------------------------------------------- products
 
-# skinny forms, the three tiles, ragged in every size
+# skinny forms, the three tiles, ragged in every size; then contractions over many stages and
+# scale groups in each tile, odd numbers of 128-element steps, the few-row forms for longer
+# contractions (2048, 4096 and 8192 are their borders) and for more rows of B (6144, 32768)
 MATMULS = [(1, 1, 1), (1, 257, 129), (5, 3, 31), (16, 100, 300), (17, 33, 128), (40, 64, 1000), (64, 130, 260),
-           (65, 70, 127), (130, 257, 1000), (300, 64, 640), (1300, 2000, 260), (2100, 5700, 200)]
+           (65, 70, 127), (130, 257, 1000), (300, 64, 640), (1300, 2000, 260), (2100, 5700, 200),
+           (90, 140, 4300), (1300, 2000, 1100), (2000, 6200, 1400), (5, 33, 2049), (16, 40, 5000), (3, 70, 8300),
+           (20, 6200, 300), (50, 6200, 700), (9, 33000, 260), (33, 32800, 130)]
 
 
 @pytest.mark.parametrize("fmts", ["e2m1 e2m1", "e2m1 e4m3", "e4m3 e2m1", "e4m3 e4m3"])
@@ -192,7 +196,8 @@ def test_linear(t, n, k, dtype, fmt):
 
 # (tokens, n, k)
 GRADS = [(1, 1, 1), (1, 70, 40), (3, 5, 129), (31, 130, 64), (64, 64, 64), (65, 127, 33), (300, 257, 100),
-         (1300, 300, 2000), (260, 1300, 2000), (2100, 90, 5700), (90, 2100, 5700)]
+         (1300, 300, 2000), (260, 1300, 2000), (2100, 90, 5700), (90, 2100, 5700), (1100, 640, 700), (700, 4096, 4096),
+         (2304, 512, 5632)]
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
@@ -305,6 +310,63 @@ def test_empty_sums_and_results():
     assert not bitopt.mx_linear_grad_weight(dy, wc, ws, 100, "e2m1", out=out).any()
     assert bitopt.mx_linear(e(0, 100, dtype=torch.bfloat16, device="cuda"), *bitopt.mx_quantize(out)).shape == (0, 7)
     assert bitopt.mx_quantize(e(0, 100, device="cuda"))[0].shape == (0, 64)
+
+
+@pytest.mark.parametrize("t", [2, 40, 100])
+def test_decoded_range_of_the_16_bit_types(t):
+    """Elements beyond fp16 are infinite in an fp16 product and exact in a bf16 one; elements
+    below bf16's normal numbers are rounded to its subnormals."""
+    n, k = 40, 64
+    w0 = np.ones((n, k))
+    w0[3] = 2.0**17
+    c, s = R.quantize(w0, "e4m3")
+    wc, ws = torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()
+    x = torch.full((t, k), 2.0**-6, dtype=torch.float16, device="cuda")
+    y = bitopt.mx_linear(x, wc, ws, "e4m3", dtype=torch.float32).cpu()
+    assert torch.isinf(y[:, 3]).all() and (y[:, :3] == 1).all() and (y[:, 4:] == 1).all()
+    y = bitopt.mx_linear(x.bfloat16(), wc, ws, "e4m3", dtype=torch.float32).cpu()
+    assert (y[:, 3] == 2.0**17).all() and (y[:, 4:] == 1).all()
+    ws[:, 0] = 2                                       # elements 1.0 (code 0x38): 2^-125, normal in bf16
+    wc[:, :32] = 0x38
+    wc[:, 32:64], ws[:, 1] = 0, 0
+    big = torch.full((t, k), 2.0**100, dtype=torch.bfloat16, device="cuda")
+    y = bitopt.mx_linear(big, wc, ws, "e4m3", dtype=torch.float32).cpu()
+    assert (y == 32 * 2.0**-25).all()
+
+
+@pytest.mark.parametrize("t", [1, 33, 90])
+def test_only_codes_of_the_matrix_are_read(t):
+    """Neighbours of an operand's memory hold NaN codes and scales: none reaches a result."""
+    n, k = 45, 300
+    rng = np.random.default_rng(4)
+
+    def between(a):
+        buf = torch.full((a.shape[0] + 2, a.shape[1]), 255, dtype=torch.uint8, device="cuda")
+        buf[1:-1] = torch.from_numpy(a).cuda()
+        return buf[1:-1]
+
+    def aligned(a):                                    # scales start 16 bytes behind the guard
+        flat = torch.full((16 + a.size + 16,), 255, dtype=torch.uint8, device="cuda")
+        flat[16:16 + a.size] = torch.from_numpy(a.reshape(-1)).cuda()
+        return flat[16:16 + a.size].view(a.shape)
+
+    for fa, fb in (("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e2m1", "e4m3"), ("e4m3", "e4m3")):
+        (ca, sa), (cb, sb) = (R.quantize(rng.standard_normal((r, k)), f) for r, f in ((t, fa), (n, fb)))
+        a, b = R.dequantize(ca, sa, k, fa), R.dequantize(cb, sb, k, fb)
+        exact = a @ b.T
+        got = bitopt.mx_matmul(between(ca), aligned(sa), between(cb), aligned(sb), k, fa, fb, dtype=torch.float32)
+        check(got, exact, R.product_bound(a, b, exact, "f32"), (fa, fb))
+    cw, sw = R.quantize(rng.standard_normal((n, k)), "e2m1")
+    w = R.dequantize(cw, sw, k, "e2m1")
+    dy = values(6, t, n, "bf16")
+    exact = host(dy) @ w
+    got = bitopt.mx_linear_grad_input(dy, between(cw), aligned(sw), k, dtype=torch.float32)
+    check(got, exact, R.product_bound(host(dy), w.T, exact, "f32"), "dx")
+    cx, sx = R.quantize(rng.standard_normal((t, k)), "e4m3")
+    x = R.dequantize(cx, sx, k, "e4m3")
+    exact = host(dy).T @ x
+    got = bitopt.mx_linear_grad_weight(dy, between(cx), aligned(sx), k)
+    check(got, exact, R.product_bound(host(dy).T, x.T, exact, "f32"), "dw")
 
 
 # --------------------------------------------------------------------------- SwiGLU
