@@ -240,10 +240,12 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // Bound: LDS.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and 32 KB
 // of writes per 32 contraction elements, 1024 cycles at 128 bytes, against 1024 cycles of
-// products; two waves a SIMD fill each other's waits.  Measured at 8192 x 8192 x 2048, bf16:
-// input grad 217 us (1270 TFLOP/s), weight grad 236 us, forward 223 us.  Writing the next
-// stage after the products instead: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic
-// is a quarter less, leave one wave a SIMD and too few registers: 360, 499, 322.
+// products; two waves a SIMD fill each other's waits.  Measured at 8192 x 8192 x 2048, bf16
+// and E2M1: input grad 225 us (1220 TFLOP/s), weight grad 232 us, forward 233 us; E4M3: 246
+// and 230 for the gradients.  The matrix pipes are busy 48% of the cycles; on zeros, which
+// let the clock rise, the forward product takes 215 us.  Writing the next stage after the
+// products instead: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter
+// less, leave one wave a SIMD and too few registers: 360, 499, 322.
 template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
@@ -370,12 +372,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // pattern, 64 separate dwords an instruction, scales were two thirds of the cache's
 // accesses: 8192 x 8192 x 8192 took 347 us.)
 //
-// Measured: 8192 x 8192 x 8192 264 us (4170 TFLOP/s), 8192 x 8192 x 2048 100 us, of which the
-// steps are 55: with one workgroup a CU, each of the four rounds of tiles begins with empty
-// buffers and ends in 128 KB of results that nothing overlaps.  Four waves of 128 x 128 that
+// Measured: 8192 x 8192 x 8192 265 us (4150 TFLOP/s), 8192 x 8192 x 2048 98 us, of which the
+// results' stores are 16 and the steps 55: with one workgroup a CU, each of the four rounds of
+// tiles begins with empty buffers and ends in 128 KB of results that nothing overlaps.  The
+// matrix instructions alone reach 9500 TFLOP/s on zeros and 7000 on random codes, where the
+// card's power sets the clock; here their pipes are busy 45% of the cycles, and the larger
+// size takes 230 us on zeros and 233 with the loads left out.  Four waves of 128 x 128 that
 // read a step's fragments under the one before took 266 and 110 us; eight such waves spill.
-// One resident grid with the next tile's loads ahead of the last one's stores took 154 us at
-// the second size, non-temporal stores 138 (against 116 at the time).
+// Reads and products of a SIMD's two waves in alternate phases, with a barrier after each: 265
+// and 100 (1024 x 4096 x 4096 16 -> 18).  One resident grid with the next tile's loads ahead of
+// the last one's stores took 154 us at the second size, non-temporal stores 138 (against 116 at
+// the time).
 
 constexpr int kGemm4K = 128;
 
