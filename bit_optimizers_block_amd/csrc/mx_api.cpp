@@ -34,9 +34,12 @@ int check_matrix(const void* p, int32_t dtype, int64_t ld, int64_t rows, int64_t
     return BITOPT_OK;
 }
 
-// A product's workgroups are counted in 31 bits (the smallest tile is 64 x 64).
-int check_tiles(int64_t rows, int64_t cols, const char* fn) {
-    if ((rows / 64 + 1) * (cols / 64 + 1) > 0x7fffffff)
+// A launch holds fewer than 2^32 threads.  Tiles of 256 x 256 take 512; smaller tiles are only
+// taken for a few hundred of them.  The form for few rows has one workgroup of 256 for 64 columns
+// where there are many.
+int check_launch(int64_t rows, int64_t cols, bool few, const char* fn) {
+    const int64_t threads = few ? (cols + 63) / 64 * 256 : (rows / 256 + 1) * (cols / 256 + 1) * 512;
+    if (threads > 0xffffffffll)
         return api_fail(BITOPT_ERR_UNSUPPORTED, "%s: %lld x %lld results are too many for one launch", fn,
                         (long long)rows, (long long)cols);
     return BITOPT_OK;
@@ -123,7 +126,7 @@ int bitopt_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_
     if (k > kMaxScaledK)
         return api_fail(BITOPT_ERR_UNSUPPORTED, "%s: k above %lld", fn, (long long)kMaxScaledK);
     if (m == 0 || n == 0) return api_status(hipSuccess, fn);
-    BITOPT_TRY(check_tiles(m, n, fn));
+    BITOPT_TRY(check_launch(m, n, m <= bitopt::kMxSkinnyRows, fn));
     BITOPT_TRY(check_matrix(out, out_dtype, ldo, m, n, "out", fn));
     if (k > 0) {
         BITOPT_TRY(check_codes(a_codes, a_scales, "a", fn));
@@ -151,7 +154,7 @@ int bitopt_mx_linear(const void* x, int32_t dtype, int64_t ldx, const uint8_t* w
     BITOPT_TRY(check_dim(n, "n", fn));
     BITOPT_TRY(check_dim(k, "k", fn));
     if (tokens == 0 || n == 0) return api_status(hipSuccess, fn);
-    BITOPT_TRY(check_tiles(tokens, n, fn));
+    BITOPT_TRY(check_launch(tokens, n, tokens <= bitopt::kMxSkinnyRows, fn));
     BITOPT_TRY(check_matrix(out, out_dtype, ldo, tokens, n, "out", fn));
     if (k > 0) {
         BITOPT_TRY(check_matrix(x, dtype, ldx, tokens, k, "x", fn));
@@ -178,7 +181,7 @@ int bitopt_mx_linear_grad_input(const void* dy, int32_t dtype, int64_t lddy, con
     BITOPT_TRY(check_dim(n, "n", fn));
     BITOPT_TRY(check_dim(k, "k", fn));
     if (tokens == 0 || k == 0) return api_status(hipSuccess, fn);
-    BITOPT_TRY(check_tiles(tokens, k, fn));
+    BITOPT_TRY(check_launch(tokens, k, false, fn));
     BITOPT_TRY(check_matrix(dx, out_dtype, lddx, tokens, k, "dx", fn));
     if (n > 0) {
         BITOPT_TRY(check_matrix(dy, dtype, lddy, tokens, n, "dy", fn));
@@ -203,7 +206,7 @@ int bitopt_mx_linear_grad_weight(const void* dy, int32_t dtype, int64_t lddy, co
     BITOPT_TRY(check_dim(n, "n", fn));
     BITOPT_TRY(check_dim(k, "k", fn));
     if (n == 0 || k == 0) return api_status(hipSuccess, fn);
-    BITOPT_TRY(check_tiles(n, k, fn));
+    BITOPT_TRY(check_launch(n, k, false, fn));
     BITOPT_TRY(check_matrix(dw, out_dtype, lddw, n, k, "dw", fn));
     if (tokens > 0) {
         BITOPT_TRY(check_matrix(dy, dtype, lddy, tokens, n, "dy", fn));

@@ -238,14 +238,14 @@ __device__ __forceinline__ void lds_barrier() {
 // is decoded and written to the other buffer between the products, and the loads of the one
 // after that are sent; the barrier that ends a stage leaves them in flight.
 //
-// Bound: LDS.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and 32 KB
-// of writes per 32 contraction elements, 1024 cycles at 128 bytes, against 1024 cycles of
-// products; two waves a SIMD fill each other's waits.  Measured at 8192 x 8192 x 2048, bf16
-// and E2M1: input grad 225 us (1220 TFLOP/s), weight grad 232 us, forward 233 us; E4M3: 246
-// and 230 for the gradients.  The matrix pipes are busy 48% of the cycles; on zeros, which
-// let the clock rise, the forward product takes 215 us.  Writing the next stage after the
-// products instead: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter
-// less, leave one wave a SIMD and too few registers: 360, 499, 322.
+// Bound: no unit alone.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and
+// 32 KB of writes through LDS per 32 contraction elements, against 1024 cycles of products;
+// counters show the matrix pipes busy 48% of the cycles and LDS 32%, the rest is waits that two
+// waves a SIMD do not fill.  Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 225 us
+// (1220 TFLOP/s), weight grad 232 us, forward 233 us (215 on zeros, which let the clock rise);
+// E4M3: 246 and 230 for the gradients.  Writing the next stage after the products instead: 304,
+// 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter less, leave one wave a SIMD
+// and too few registers: 360, 499, 322.
 template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
@@ -376,7 +376,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // results' stores are 16 and the steps 55: with one workgroup a CU, each of the four rounds of
 // tiles begins with empty buffers and ends in 128 KB of results that nothing overlaps.  The
 // matrix instructions alone reach 9500 TFLOP/s on zeros and 7000 on random codes, where the
-// card's power sets the clock; here their pipes are busy 45% of the cycles, and the larger
+// card's power sets the clock; here their pipes are busy 47% of the cycles, LDS 27%, and the larger
 // size takes 230 us on zeros and 233 with the loads left out.  Four waves of 128 x 128 that
 // read a step's fragments under the one before took 266 and 110 us; eight such waves spill.
 // Reads and products of a SIMD's two waves in alternate phases, with a barrier after each: 265

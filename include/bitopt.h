@@ -511,7 +511,8 @@ BITOPT_API int bitopt_step_multi(const bitopt_hparams* hp, int32_t step, const b
  *     length when there is more than one row); a row's elements are contiguous and need
  *     only their own alignment.
  *   - A size of zero gives a successful call: without results nothing is done, and a
- *     product over no elements is zero.  Sizes above 2^30 give UNSUPPORTED.
+ *     product over no elements is zero.  Sizes above 2^30 give UNSUPPORTED, and so do products
+ *     that one launch does not hold: some 2^39 results, or 2^30 - 63 columns for up to 64 rows.
  *   - Inputs and results must not overlap, except that bitopt_swiglu_backward_mx8 may write
  *     dgate or dup over dy when both have the same rows.
  *   - No call needs a workspace, waits or allocates; every call may be captured into a HIP

@@ -148,6 +148,10 @@ def test_refused(B, call, args, text):
     (grad_weight, dict(dtype=0)), (grad_weight, dict(tokens=2**30 + 1)), (swiglu_forward, dict(rows=2**33)),
     (linear, dict(tokens=2**30, n=2**30, ldo=2**30)), (grad_input, dict(tokens=2**30, k=2**30, ldo=2**30)),
     (grad_weight, dict(n=2**30, k=2**30, ldo=2**30)),
+    # 2^32 threads and more in one launch: few rows, and the smallest such grid of large tiles
+    (matmul, dict(m=17, n=2**30, ldo=2**30)), (linear, dict(tokens=64, n=2**30 - 63, ldo=2**30)),
+    (linear, dict(tokens=2**20, n=2**19, ldo=2**19)), (grad_input, dict(tokens=2**21 - 256, k=2**18, ldo=2**18)),
+    (grad_weight, dict(n=2**19, k=2**20, ldo=2**20)),
 ])
 def test_unsupported(B, call, args):
     assert call(B.lib(), **args) == B.ERR_UNSUPPORTED and B.last_error()
