@@ -242,7 +242,8 @@ __global__ __launch_bounds__(WAVES * 64) void k_mx_skinny(MxGemmArgs g) {
 // Up to 16 rows of A and a contraction that the waves hold at four chunks each: A's
 // fragments are loaded once and stay in registers, and a workgroup goes through tiles of 16
 // rows of B, the next tile's codes on their way while one is multiplied (one row against
-// 50257 x 2048: 16.3 us, against 20.8 with A's rows loaded for every tile).
+// 50257 x 2048: 16.3 us, against 20.8 with A's rows loaded for every tile;
+// registers for a fourth wave a SIMD spill: 24).
 template <int DT, int XSRC, int FMT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_mx_tokens(MxGemmArgs g) {
     constexpr bool scaled = XSRC == kXE2M1 && FMT == kMxE2M1;
