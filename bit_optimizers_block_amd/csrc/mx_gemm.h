@@ -35,7 +35,7 @@ constexpr int kGemmK = 64;      // contraction elements per LDS stage of the 16-
 // c ^ (r & 7), so the 16 rows of a fragment read fall on different banks.  Across: kGemmK
 // rows of 2R bytes and 32 of padding, so the four rows of a transpose read do (a swizzle of
 // the segments does the same, but costs a register of addresses for every fragment).
-template <int DT, int SRC, int R, int NT> struct MxStage {
+template <int DT, int SRC, int R, int NT, bool WHOLE> struct MxStage {
     static constexpr bool along = mx_is_along(SRC), codes = mx_is_codes(SRC), four = mx_is_4bit(SRC);
     // elements per thread item: one 16-byte load, or one of 8 where a small tile's 4-bit codes
     // would leave half of the workgroup without
@@ -61,11 +61,13 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     // themselves.
     static constexpr bool own_scales = codes && !along;
     static constexpr int SCALES = codes && along ? R * 16 : 0;
-    // Where a 16-bit operand's memory rows end in a stage, an item is one load of the row's last
-    // eight elements at most, and store() shifts it and zeroes what lies beyond (read element
-    // by element, a ragged edge waited for every one: 777 x 1001 x 513 weight gradient 15 us).
-    static constexpr bool SHIFTS = !codes;
-    int span;               // elements of a memory row: all of them (along), from the tile's first (across)
+    // WHOLE: every stage of every tile lies inside the operand and its offsets fit, so nothing is
+    // looked at on the way.  Otherwise a stage over an edge takes load_any().  Along, that is the
+    // last stage only, and its items are shifted as they are loaded.  Across, a ragged tile has
+    // one in every stage: an item is one load of the row's last eight elements at most, and
+    // store() shifts it and zeroes what lies beyond, so the load stays in flight.
+    static constexpr bool SHIFTS = !codes && !along && !WHOLE;
+    int span;               // elements of a memory row from the tile's first (across)
     uint32_t off[OFFS], soff;
     u32x4 raw[N];
     uint32_t scale[own_scales ? N : 1];
@@ -79,18 +81,24 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
         }
     }
     // rows: the operand's rows (columns, if across); r0: the tile's first
-    __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int K, int r0, int tid) {
-        span = along ? K : rows - r0;
+    __device__ __forceinline__ void init(int64_t ld, int64_t ld_sc, int rows, int r0, int tid) {
+        span = rows - r0;
 #pragma unroll
         for (int i = 0; i < OFFS; ++i) {
             const int idx = min(i * NT + tid, ITEMS - 1);
             const int a = idx / PER_ROW;
             int b = idx % PER_ROW * EL;
-            if constexpr (SHIFTS && !along) b = max(0, min(b, rows - r0 - 8));
+            if constexpr (SHIFTS) b = max(0, min(b, rows - r0 - 8));
             const uint32_t row = along ? (uint32_t)min(a, rows - 1 - r0) : (uint32_t)a;
             off[i] = row * (uint32_t)(codes ? ld : 2 * ld) + (codes ? (four ? b / 2 : b) : 2 * b);
             if constexpr (own_scales) soff = row * (uint32_t)ld_sc + b / kMxBlock;
         }
+    }
+    // Whether every stage of every tile is inside().
+    static bool whole(int64_t ld, int64_t rows, int64_t K) {
+        if (ld >= (1 << 22)) return false;
+        if (along) return codes || K % kGemmK == 0;
+        return K % kGemmK == 0 && (rows + R - 1) / R * R <= (codes ? mx_padded(rows) : rows);
     }
     // Whether the stage from k0 lies inside the operand and its offsets fit (wave-uniform).
     static __device__ __forceinline__ bool inside(int64_t ld, int rows, int K, int r0, int k0) {
@@ -120,7 +128,10 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
                                              int K, int r0, int k0, int tid) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int idx = i * NT + tid;
+            // computed here each time: ahead of the loop, the addresses of all items would take
+            // registers in every stage
+            int idx = i * NT + tid;
+            asm volatile("" : "+v"(idx));
             const int a = idx / PER_ROW, b = idx % PER_ROW * EL;
             raw[i] = u32x4{0u, 0u, 0u, 0u};
             if constexpr (own_scales) scale[i] = 0u;
@@ -129,16 +140,13 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
             const int64_t row = along ? min(r0 + a, rows - 1) : k0 + a;
             const int col = (along ? k0 : r0) + b;
             if constexpr (!codes) {
-                if (span >= 8) {
-                    if (along || row < K)
-                        raw[i] = ld16_a2(reinterpret_cast<const uint16_t*>(base) + row * ld +
-                                         min(col, (along ? K : rows) - 8));
-                    continue;
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + row * ld;
+                if constexpr (along) {
+                    raw[i] = ld_half8(p + col, K - col, col);
+                } else if (row < K) {           // rows past the contraction are zero
+                    if (span >= 8) raw[i] = ld16_a2(p + min(col, rows - 8));
+                    else raw[i] = ld_half8(p + col, rows - col, 0);
                 }
-                // elements left in the row: beyond it, and on rows past the contraction, zero
-                const int left = along ? K - col : (row < K ? rows - col : 0);
-                if (left > 0)
-                    raw[i] = ld_half8(reinterpret_cast<const uint16_t*>(base) + row * ld + col, left, 0);
             } else {
                 // rows of codes are padded with zeros to 128 elements
                 const int width = (int)mx_padded(along ? K : rows);
@@ -151,7 +159,7 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
     }
     __device__ __forceinline__ void load(const void* base, int64_t ld, const uint8_t* sc, int64_t ld_sc, int rows, int K,
                                          int r0, int k0, int tid) {
-        if (inside(ld, rows, K, r0, k0)) load_inside(base, ld, sc, ld_sc, r0, k0);
+        if (WHOLE || inside(ld, rows, K, r0, k0)) load_inside(base, ld, sc, ld_sc, r0, k0);
         else load_any(base, ld, sc, ld_sc, rows, K, r0, k0, tid);
     }
 
@@ -179,10 +187,11 @@ template <int DT, int SRC, int R, int NT> struct MxStage {
         u32x4 v;
         if constexpr (!codes) {
             v = raw[i];
-            const int end = along ? span - s * kGemmK : span;
-            if (span >= 8 && end < (along ? kGemmK : R)) {
-                const int left = end - c * 8;
-                v = left >= 8 ? v : left > 0 ? half_shift(v, 8 - left) : u32x4{0u, 0u, 0u, 0u};
+            if constexpr (SHIFTS) {
+                if (span >= 8 && span < R) {
+                    const int left = span - c * 8;
+                    v = left >= 8 ? v : left > 0 ? half_shift(v, 8 - left) : u32x4{0u, 0u, 0u, 0u};
+                }
             }
         } else {
             uint32_t b;
@@ -241,16 +250,15 @@ __device__ __forceinline__ void lds_barrier() {
 // Bound: no unit alone.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and
 // 32 KB of writes through LDS per 32 contraction elements, against 1024 cycles of products;
 // counters show the matrix pipes busy 48% of the cycles and LDS 32%, the rest is waits that two
-// waves a SIMD do not fill.  Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 225 us
-// (1220 TFLOP/s), weight grad 232 us, forward 233 us (215 on zeros, which let the clock rise);
-// E4M3: 246 and 230 for the gradients.  Writing the next stage after the products instead: 304,
-// 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter less, leave one wave a SIMD
+// waves a SIMD do not fill.  Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 203 us
+// (1350 TFLOP/s), weight grad 215 us, forward 212 us; E4M3: 209, 208 and 221.  Writing the next
+// stage after the products instead, in an earlier form: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter less, leave one wave a SIMD
 // and too few registers: 360, 499, 322.
-template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN>
+template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN, bool WHOLE>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
-    using SA = MxStage<DT, ASRC, BM, NT>;
-    using SB = MxStage<DT, BSRC, BN, NT>;
+    using SA = MxStage<DT, ASRC, BM, NT, WHOLE>;
+    using SB = MxStage<DT, BSRC, BN, NT, WHOLE>;
     constexpr int STAGE = SA::BYTES + SB::BYTES, SCALES = SA::SCALES + SB::SCALES;
     __shared__ __attribute__((aligned(16))) char lds[2 * STAGE + 2 * SCALES];
 
@@ -264,8 +272,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 
     SA sa;
     SB sb;
-    sa.init(lda, g.a_row_scales, g.M, g.K, m0, tid);
-    sb.init(g.b_row_bytes, g.b_row_scales, g.N, g.K, n0, tid);
+    sa.init(lda, g.a_row_scales, g.M, m0, tid);
+    sb.init(g.b_row_bytes, g.b_row_scales, g.N, n0, tid);
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -539,21 +547,26 @@ hipError_t mx_by_tile(const MxGemmArgs& g, Big big, Mid mid, Small small) {
     return small(dim3((unsigned)tiles(64)));
 }
 
+// Sizes whose every stage lies inside both operands take the form that looks for no edge: us
+// general and whole, bf16, 8192 x 8192 x 2048: forward E2M1 220, 212, E4M3 251, 221; weight grad
+// 233, 215 and 227, 208; 512 x 2048 x 2048 forward 14.3, 12.7.  Input grad is alike in both.
+template <int DT, int ASRC, int BSRC, int T, int WM, int WN>
+hipError_t mx_gemm16_tile(const MxGemmArgs& g, dim3 grid, hipStream_t s) {
+    constexpr int threads = (T / WM) * (T / WN) * 64;
+    using SA = MxStage<DT, ASRC, T, threads, true>;
+    using SB = MxStage<DT, BSRC, T, threads, true>;
+    if (SA::whole(SA::codes ? g.a_row_bytes : g.lda, g.M, g.K) && SB::whole(g.b_row_bytes, g.N, g.K))
+        hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, T, T, WM, WN, true>), grid, dim3(threads), 0, s, g);
+    else
+        hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, T, T, WM, WN, false>), grid, dim3(threads), 0, s, g);
+    return hipGetLastError();
+}
+
 template <int DT, int ASRC, int BSRC> hipError_t mx_gemm16(const MxGemmArgs& g, hipStream_t s) {
     return mx_by_tile(
-        g,
-        [&](dim3 grid) {
-            hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, 256, 256, 128, 64>), grid, dim3(512), 0, s, g);
-            return hipGetLastError();
-        },
-        [&](dim3 grid) {
-            hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, 128, 128, 64, 32>), grid, dim3(512), 0, s, g);
-            return hipGetLastError();
-        },
-        [&](dim3 grid) {
-            hipLaunchKernelGGL((k_mx_gemm16<DT, ASRC, BSRC, 64, 64, 32, 32>), grid, dim3(256), 0, s, g);
-            return hipGetLastError();
-        });
+        g, [&](dim3 grid) { return mx_gemm16_tile<DT, ASRC, BSRC, 256, 128, 64>(g, grid, s); },
+        [&](dim3 grid) { return mx_gemm16_tile<DT, ASRC, BSRC, 128, 64, 32>(g, grid, s); },
+        [&](dim3 grid) { return mx_gemm16_tile<DT, ASRC, BSRC, 64, 32, 32>(g, grid, s); });
 }
 
 }  // namespace bitopt
