@@ -766,7 +766,7 @@ def mx_linear_grad_weight(dy, x_codes, x_scales, k: int, fmt: str = "e4m3", out=
 
 def swiglu_save8(gate, up, y=None, saved=None, stream=None):
     """gate * sigmoid(gate) * up, and its inputs in 8 bits for swiglu_backward8: (y, saved),
-    saved = (gate_codes, gate_scales, up_codes, up_scales) in MX E4M3."""
+    saved = (gate_codes, gate_scales, up_codes, up_scales) in MX E4M3.  y may be gate or up."""
     rows, cols, ldg = _rows(gate, "gate")
     dt, device, dtype = _dt(gate), gate.device, gate.dtype
     urows, ucols, ldu = _rows(up, "up", device)
@@ -788,7 +788,7 @@ def swiglu_save8(gate, up, y=None, saved=None, stream=None):
 
 
 def swiglu_backward8(dy, saved, dgate=None, dup=None, stream=None):
-    """(dgate, dup) of swiglu_save8 from dy and what it saved."""
+    """(dgate, dup) of swiglu_save8 from dy and what it saved.  dgate or dup may be dy."""
     rows, cols, lddy = _rows(dy, "dy")
     dt, device, dtype = _dt(dy), dy.device, dy.dtype
     gc, gs, uc, us = saved

@@ -2,6 +2,7 @@
 // checks and dispatch.
 #include "bitopt.h"
 #include "launch.h"
+#include "mx_overlap.h"
 
 namespace {
 
@@ -64,6 +65,35 @@ int check_half(int32_t dtype, const char* fn) {
     return BITOPT_OK;
 }
 
+// A matrix of a call, for the check that results share no memory with anything else of it.
+struct Named {
+    const char* name;
+    bitopt::ByteRows at;
+};
+Named elements(const char* name, const void* p, int32_t dtype, int64_t ld, int64_t rows, int64_t cols) {
+    const int64_t es = dtype == BITOPT_F32 ? 4 : 2;
+    // distances beyond 2^60 elements are no memory: one that still fits 64 bits stands for them
+    return {name, {p, rows, cols * es, std::min<int64_t>(ld, int64_t{1} << 60) * es}};
+}
+Named packed(const char* name, const void* p, int64_t rows, int64_t width) { return {name, {p, rows, width, width}}; }
+
+// The first `results` of the matrices are written: none may meet another.  The first `in_place` of
+// those are laid out as the read matrices at `over` or `over2` and written item by item after the
+// reads of the same items, so they may lie over the very same rows.
+template <size_t N> int check_apart(const char* fn, size_t results, const Named (&m)[N], size_t in_place = 0,
+                                    const void* over = nullptr, const void* over2 = nullptr) {
+    for (size_t r = 0; r < results; ++r)
+        for (size_t i = r + 1; i < N; ++i) {
+            const bitopt::ByteRows &a = m[r].at, &b = m[i].at;
+            if (!bitopt::rows_meet(a, b)) continue;
+            if (r < in_place && i >= results && a.p == b.p && (b.p == over || b.p == over2) &&
+                (a.rows == 1 || a.stride == b.stride))
+                continue;
+            return api_fail(BITOPT_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, m[r].name, m[i].name);
+        }
+    return BITOPT_OK;
+}
+
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
@@ -94,6 +124,9 @@ int bitopt_mx_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols,
     if (rows == 0 || cols == 0) return api_status(hipSuccess, fn);
     BITOPT_TRY(check_matrix(x, dtype, ldx, rows, cols, "x", fn));
     BITOPT_TRY(check_codes(codes, scales, "x", fn));
+    BITOPT_TRY(check_apart(fn, 2, {packed("codes", codes, rows, bitopt::mx_code_bytes(cols, format)),
+                                   packed("scales", scales, rows, bitopt::mx_scale_bytes(cols)),
+                                   elements("x", x, dtype, ldx, rows, cols)}));
     bitopt::MxCodecArgs a{};
     a.x = x; a.ldx = ldx; a.codes = codes; a.scales = scales; a.rows = rows; a.cols = cols;
     return api_status(bitopt::launch_mx_quantize(a, dtype, format, as_stream(stream)), fn);
@@ -108,6 +141,9 @@ int bitopt_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t fo
     if (rows == 0 || cols == 0) return api_status(hipSuccess, fn);
     BITOPT_TRY(check_codes(codes, scales, "the input", fn));
     BITOPT_TRY(check_matrix(out, dtype, ldo, rows, cols, "out", fn));
+    BITOPT_TRY(check_apart(fn, 1, {elements("out", out, dtype, ldo, rows, cols),
+                                   packed("codes", codes, rows, bitopt::mx_code_bytes(cols, format)),
+                                   packed("scales", scales, rows, bitopt::mx_scale_bytes(cols))}));
     bitopt::MxCodecArgs a{};
     a.out = out; a.ldo = ldo; a.rows = rows; a.cols = cols;
     a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
@@ -131,6 +167,11 @@ int bitopt_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_
     if (k > 0) {
         BITOPT_TRY(check_codes(a_codes, a_scales, "a", fn));
         BITOPT_TRY(check_codes(b_codes, b_scales, "b", fn));
+        BITOPT_TRY(check_apart(fn, 1, {elements("out", out, out_dtype, ldo, m, n),
+                                       packed("a", a_codes, m, bitopt::mx_code_bytes(k, a_format)),
+                                       packed("a's scales", a_scales, m, bitopt::mx_scale_bytes(k)),
+                                       packed("b", b_codes, n, bitopt::mx_code_bytes(k, b_format)),
+                                       packed("b's scales", b_scales, n, bitopt::mx_scale_bytes(k))}));
     }
     MxGemmArgs g{};
     g.a = a_codes; g.a_scales = a_scales; g.b = b_codes; g.b_scales = b_scales;
@@ -159,6 +200,10 @@ int bitopt_mx_linear(const void* x, int32_t dtype, int64_t ldx, const uint8_t* w
     if (k > 0) {
         BITOPT_TRY(check_matrix(x, dtype, ldx, tokens, k, "x", fn));
         BITOPT_TRY(check_codes(w_codes, w_scales, "w", fn));
+        BITOPT_TRY(check_apart(fn, 1, {elements("out", out, out_dtype, ldo, tokens, n),
+                                       elements("x", x, dtype, ldx, tokens, k),
+                                       packed("w", w_codes, n, bitopt::mx_code_bytes(k, format)),
+                                       packed("w's scales", w_scales, n, bitopt::mx_scale_bytes(k))}));
     }
     MxGemmArgs g{};
     g.a = x; g.lda = ldx; g.b = w_codes; g.b_scales = w_scales;
@@ -186,6 +231,10 @@ int bitopt_mx_linear_grad_input(const void* dy, int32_t dtype, int64_t lddy, con
     if (n > 0) {
         BITOPT_TRY(check_matrix(dy, dtype, lddy, tokens, n, "dy", fn));
         BITOPT_TRY(check_codes(w_codes, w_scales, "w", fn));
+        BITOPT_TRY(check_apart(fn, 1, {elements("dx", dx, out_dtype, lddx, tokens, k),
+                                       elements("dy", dy, dtype, lddy, tokens, n),
+                                       packed("w", w_codes, n, bitopt::mx_code_bytes(k, format)),
+                                       packed("w's scales", w_scales, n, bitopt::mx_scale_bytes(k))}));
     }
     MxGemmArgs g{};
     g.a = dy; g.lda = lddy; g.b = w_codes; g.b_scales = w_scales;
@@ -211,6 +260,10 @@ int bitopt_mx_linear_grad_weight(const void* dy, int32_t dtype, int64_t lddy, co
     if (tokens > 0) {
         BITOPT_TRY(check_matrix(dy, dtype, lddy, tokens, n, "dy", fn));
         BITOPT_TRY(check_codes(x_codes, x_scales, "x", fn));
+        BITOPT_TRY(check_apart(fn, 1, {elements("dw", dw, out_dtype, lddw, n, k),
+                                       elements("dy", dy, dtype, lddy, tokens, n),
+                                       packed("x", x_codes, tokens, bitopt::mx_code_bytes(k, format)),
+                                       packed("x's scales", x_scales, tokens, bitopt::mx_scale_bytes(k))}));
     }
     MxGemmArgs g{};
     g.a = dy; g.lda = lddy; g.b = x_codes; g.b_scales = x_scales;
@@ -233,6 +286,14 @@ int bitopt_swiglu_forward_mx8(const void* gate, const void* up, int32_t dtype, i
     BITOPT_TRY(check_matrix(y, dtype, ldy, rows, cols, "y", fn));
     BITOPT_TRY(check_codes(gate_codes, gate_scales, "gate", fn));
     BITOPT_TRY(check_codes(up_codes, up_scales, "up", fn));
+    BITOPT_TRY(check_apart(
+        fn, 5,
+        {elements("y", y, dtype, ldy, rows, cols), packed("gate's codes", gate_codes, rows, bitopt::mx_code_bytes(cols, BITOPT_MX_E4M3)),
+         packed("gate's scales", gate_scales, rows, bitopt::mx_scale_bytes(cols)),
+         packed("up's codes", up_codes, rows, bitopt::mx_code_bytes(cols, BITOPT_MX_E4M3)),
+         packed("up's scales", up_scales, rows, bitopt::mx_scale_bytes(cols)),
+         elements("gate", gate, dtype, ldg, rows, cols), elements("up", up, dtype, ldu, rows, cols)},
+        1, gate, up));
     bitopt::SwigluArgs a{};
     a.gate = gate; a.up = up; a.y = y; a.ldg = ldg; a.ldu = ldu; a.ldy = ldy;
     a.gate_codes = gate_codes; a.gate_scales = gate_scales; a.up_codes = up_codes; a.up_scales = up_scales;
@@ -254,6 +315,14 @@ int bitopt_swiglu_backward_mx8(const void* dy, int32_t dtype, int64_t rows, int6
     BITOPT_TRY(check_matrix(dup, dtype, lddu, rows, cols, "dup", fn));
     BITOPT_TRY(check_codes(gate_codes, gate_scales, "gate", fn));
     BITOPT_TRY(check_codes(up_codes, up_scales, "up", fn));
+    BITOPT_TRY(check_apart(
+        fn, 2,
+        {elements("dgate", dgate, dtype, lddg, rows, cols), elements("dup", dup, dtype, lddu, rows, cols),
+         elements("dy", dy, dtype, lddy, rows, cols), packed("gate's codes", gate_codes, rows, bitopt::mx_code_bytes(cols, BITOPT_MX_E4M3)),
+         packed("gate's scales", gate_scales, rows, bitopt::mx_scale_bytes(cols)),
+         packed("up's codes", up_codes, rows, bitopt::mx_code_bytes(cols, BITOPT_MX_E4M3)),
+         packed("up's scales", up_scales, rows, bitopt::mx_scale_bytes(cols))},
+        2, dy));
     bitopt::SwigluArgs a{};
     a.dy = dy; a.ldy = lddy; a.dgate = dgate; a.lddg = lddg; a.dup = dup; a.lddu = lddu;
     a.gate_codes = const_cast<uint8_t*>(gate_codes); a.gate_scales = const_cast<uint8_t*>(gate_scales);

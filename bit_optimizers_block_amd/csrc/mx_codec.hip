@@ -192,7 +192,9 @@ template <int DT> __device__ __forceinline__ float sigmoid(float g) {
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// y = gate * sigmoid(gate) * up, and both inputs in MX E4M3.
+// y = gate * sigmoid(gate) * up, and both inputs in MX E4M3.  y may lie over gate or up (and in
+// the backward pass dgate or dup over dy): a lane reads its item before it writes it, and what the
+// last item's load takes from the item before is shifted out.
 template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_forward(SwigluArgs a, RowGrid g) {
     const int64_t padded = mx_padded(a.cols);
     for_items(g, a.rows, (int32_t)(padded / kPer<DT>), [&](int64_t row, int32_t item) {

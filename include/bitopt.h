@@ -513,8 +513,10 @@ BITOPT_API int bitopt_step_multi(const bitopt_hparams* hp, int32_t step, const b
  *   - A size of zero gives a successful call: without results nothing is done, and a
  *     product over no elements is zero.  Sizes above 2^30 give UNSUPPORTED, and so do products
  *     that one launch does not hold: some 2^39 results, or 2^30 - 63 columns for up to 64 rows.
- *   - Inputs and results must not overlap, except that bitopt_swiglu_backward_mx8 may write
- *     dgate or dup over dy when both have the same rows.
+ *   - A result that shares memory with an input or with another result gives INVALID_ARG;
+ *     rows that lie between another matrix's rows, as halves of a wider buffer, do not.  Two
+ *     calls take the very rows of an input for a result: bitopt_swiglu_forward_mx8 may write
+ *     y over gate or up, and bitopt_swiglu_backward_mx8 dgate or dup over dy.
  *   - No call needs a workspace, waits or allocates; every call may be captured into a HIP
  *     graph and gives the same bits on every run.
  */

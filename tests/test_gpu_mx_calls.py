@@ -1,0 +1,72 @@
+"""GPU: how the MX operators are called -- results over and between other matrices, streams of any
+kind -- through the binding."""
+import pytest
+import torch
+
+from bit_optimizers_block_amd import bitopt
+from test_gpu_mx import DT, padded_rows, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    bitopt.lib()
+
+
+def raises(call, text):
+    with pytest.raises(bitopt.BitoptError, match=text):
+        call()
+
+
+def test_results_over_other_matrices_are_refused():
+    x = values(1, 70, 128, "bf16")
+    q, q8 = bitopt.mx_quantize(x), bitopt.mx_quantize(x, "e4m3")
+    w = bitopt.mx_quantize(values(2, 128, 128, "f32"))
+    raises(lambda: bitopt.mx_linear(x, *w, out=x), "out overlaps x")
+    raises(lambda: bitopt.mx_linear_grad_input(x, *w, 128, out=x), "dx overlaps dy")
+    raises(lambda: bitopt.mx_linear_grad_input(x[:40], *w, 128, out=x[30:]), "dx overlaps dy")
+    square = values(3, 128, 128, "bf16")
+    raises(lambda: bitopt.mx_linear_grad_weight(square, *bitopt.mx_quantize(square, "e4m3"), 128, out=square),
+           "dw overlaps dy")
+    raises(lambda: bitopt.mx_quantize(x, "e4m3", codes=x.view(torch.uint8).view(-1)[:70 * 128].view(70, 128)), "overlaps x")
+    raises(lambda: bitopt.mx_dequantize(q8[0][:16], q8[1][:16], 128, "e4m3",
+                                        out=q8[0][:32].view(-1).view(torch.bfloat16).view(16, 128)), "out overlaps codes")
+    raises(lambda: bitopt.mx_matmul(q[0][:1], q[1][:1], w[0][:8], w[1][:8], 128, out=w[0][:1, :16].view(torch.bfloat16)),
+           "out overlaps b")
+    y, saved = bitopt.swiglu_save8(x, x)
+    raises(lambda: bitopt.swiglu_save8(x, x, saved=(saved[0], saved[1], saved[0], saved[3])), "overlaps up's codes")
+    raises(lambda: bitopt.swiglu_save8(x[:-1], x[:-1], y=x[1:]), "y overlaps")
+    g = torch.empty_like(x)
+    raises(lambda: bitopt.swiglu_backward8(x, saved, dgate=g, dup=g), "dgate overlaps dup")
+    raises(lambda: bitopt.swiglu_backward8(x, saved, dgate=x, dup=x), "dgate overlaps dup")
+    assert torch.equal(y, bitopt.swiglu_save8(x, x)[0])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,cols", [(1, 7), (33, 205), (70, 512)])
+def test_results_between_and_over_inputs(rows, cols, dtype):
+    """Gate and up, and their gradients, as halves of one buffer; y over gate or up; dgate or dup
+    over dy."""
+    both = values(1, rows, 2 * cols, dtype)
+    gate, up = both[:, :cols], both[:, cols:]
+    dy = values(2, rows, cols, dtype)
+    y, saved = bitopt.swiglu_save8(gate.contiguous(), up.contiguous())
+    dgate, dup = bitopt.swiglu_backward8(dy, saved)
+    grads = torch.empty_like(both)
+    bitopt.swiglu_backward8(dy, saved, dgate=grads[:, :cols], dup=grads[:, cols:])
+    assert torch.equal(grads, torch.cat((dgate, dup), 1))
+    wide = torch.full((rows, 3 * cols), 9.0, dtype=DT[dtype], device="cuda")
+    wide[:, :2 * cols] = both
+    same = bitopt.swiglu_save8(wide[:, :cols], wide[:, cols:2 * cols], y=wide[:, 2 * cols:])
+    assert torch.equal(same[0], y) and all(torch.equal(a, b) for a, b in zip(same[1], saved))
+    for over in range(2):
+        a, b = padded_rows(gate, 3, 1), padded_rows(up, 3, 1)
+        same = bitopt.swiglu_save8(a, b, y=(a, b)[over])
+        assert torch.equal(same[0], y) and all(torch.equal(u, v) for u, v in zip(same[1], saved))
+        d, other = padded_rows(dy, 5, 1), torch.empty_like(dy)
+        pair = (d, other) if over == 0 else (other, d)
+        bitopt.swiglu_backward8(d, saved, dgate=pair[0], dup=pair[1])
+        assert torch.equal(pair[0], dgate) and torch.equal(pair[1], dup)
