@@ -4,6 +4,7 @@ lengths at which the forms change."""
 import pytest
 import torch
 
+import mx_reference as R
 import mx_sums as S
 from bit_optimizers_block_amd import bitopt
 
@@ -106,3 +107,62 @@ def test_gradients(m, n, k, dtype, fmt):
     v = v.to(DT[dtype]).double()
     near(bitopt.mx_linear_grad_input(d, *q, n, fmt, dtype=torch.float32), d.double(), v.T, k)
     near(bitopt.mx_linear_grad_weight(d.t().contiguous(), *q, n, fmt), d.double(), v.T, k)
+
+
+# ------------------------------------------- elements below the normal numbers of 16 bits
+
+def small(seed, rows, cols, fmt, dtype):
+    """Random codes under scales that put most elements below `dtype`'s normal numbers, many below
+    its smallest step or half way between two; as an MX matrix, and as values rounded to
+    `dtype`.  In units of the smallest step (2^-133, 2^-24) an element is at most 448 2^7 < 2^16,
+    so sums of up to 2^8 of them times one power of two are exact in fp32."""
+    g = torch.Generator()
+    g.manual_seed(seed)
+    kp = (cols + 127) // 128 * 128
+    codes = torch.randint(0, 256, (rows, kp // (2 if fmt == "e2m1" else 1)), generator=g, dtype=torch.uint8)
+    if fmt == "e4m3":
+        codes[(codes & 127) == 127] = 1                 # no NaN
+        codes[:, cols:] = 0
+    else:
+        full = torch.stack((codes & 15, codes >> 4), 2).view(rows, -1)
+        full[:, cols:] = 0
+        codes = full[:, 0::2] | full[:, 1::2] << 4
+    low = {"f16": 127 - 24, "bf16": 0}[dtype]
+    scales = low + torch.randint(0, 2, (rows, kp // 32), generator=g, dtype=torch.uint8)
+    scales[:, (cols + 31) // 32:] = 0
+    v = torch.from_numpy(R.dequantize(codes.numpy(), scales.numpy(), cols, fmt))
+    r = v.float().to(DT[dtype])                         # exact in fp32, then rounded to nearest even
+    below = r.float().abs() < torch.finfo(DT[dtype]).tiny
+    assert below.float().mean() > 0.2 and (r[below] != 0).any()
+    # E2M1's least element is 2^-128, above bf16's smallest step: nothing is rounded there
+    assert rows == 1 or (r.double() != v).any() == ((fmt, dtype) != ("e2m1", "bf16"))
+    return (codes.cuda(), scales.cuda()), r.double().cuda()
+
+
+def signs(seed, rows, cols, dtype):
+    """One power of two with random signs, large enough that products are normal in fp32."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = (torch.randint(0, 2, (rows, cols), generator=g, device="cuda").double() * 2 - 1)
+    return x * {"f16": 2.0**12, "bf16": 2.0**100}[dtype]
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t", [1, 24, 60, 70, 200])
+def test_elements_below_the_normal_numbers(t, dtype, fmt):
+    n, k = 90, 130
+    q, w = small(1, n, k, fmt, dtype)
+    x, dy = signs(2, t, k, dtype), signs(3, t, n, dtype)
+    same(bitopt.mx_linear(x.to(DT[dtype]), *q, fmt, dtype=torch.float32), x @ w.T)
+    same(bitopt.mx_linear_grad_input(dy.to(DT[dtype]), *q, k, fmt, dtype=torch.float32), dy @ w)
+    q, v = small(4, t, k, fmt, dtype)
+    same(bitopt.mx_linear_grad_weight(dy.to(DT[dtype]), *q, k, fmt), dy.T @ v)
+    if dtype == "bf16":                                 # products of two MX matrices decode to bf16
+        q, w = small(5, n, k, fmt, dtype)
+        for fa in ("e2m1", "e4m3"):
+            qa, a = mx(x, fa)
+            assert torch.equal(a, x)
+            if fa == fmt == "e2m1":                     # multiplied as codes: nothing is rounded
+                w = torch.from_numpy(R.dequantize(q[0].cpu().numpy(), q[1].cpu().numpy(), k, fmt)).cuda()
+            same(bitopt.mx_matmul(*qa, *q, k, fa, fmt, dtype=torch.float32), x @ w.T)
