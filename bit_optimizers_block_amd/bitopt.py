@@ -631,6 +631,9 @@ def _elsewhere(device, stream):
     inside then belong to the stream that writes them."""
     if stream is None:
         return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):       # any object with a stream's handle
+        handle = int(stream.cuda_stream or 0)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the arguments on {device}")
     return torch.cuda.stream(stream)

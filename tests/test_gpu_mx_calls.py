@@ -70,3 +70,52 @@ def test_results_between_and_over_inputs(rows, cols, dtype):
         pair = (d, other) if over == 0 else (other, d)
         bitopt.swiglu_backward8(d, saved, dgate=pair[0], dup=pair[1])
         assert torch.equal(pair[0], dgate) and torch.equal(pair[1], dup)
+
+
+class Handle:
+    """A stream of another library: what the step and codec calls take too."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("given", ["own", "default"])
+def test_streams_of_other_libraries(monkeypatch, given):
+    """Any object with a stream's handle: the work goes to that very stream."""
+    x, gate = values(1, 70, 130, "bf16"), values(2, 70, 90, "bf16")
+    w = bitopt.mx_quantize(values(3, 90, 130, "f32"))
+    q = bitopt.mx_quantize(x, "e4m3")
+    want = [bitopt.mx_linear(x, *w), bitopt.mx_linear_grad_input(gate, *w, 130), bitopt.mx_linear_grad_weight(gate, *q, 130),
+            bitopt.mx_matmul(*q, *w, 130, "e4m3"), bitopt.mx_dequantize(*q, 130, "e4m3"), bitopt.swiglu_save8(gate, gate)[0]]
+    torch.cuda.synchronize()
+    own = torch.cuda.Stream() if given == "own" else torch.cuda.default_stream()
+    handle, seen, real = Handle(own), [], bitopt.lib()
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                seen.append(args[-1])
+                return getattr(real, name)(*args)
+            return call if name.startswith(("bitopt_mx", "bitopt_swiglu")) else getattr(real, name)
+    monkeypatch.setattr(bitopt, "lib", Library)
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):                      # neither the current stream nor the default one
+        got = [bitopt.mx_linear(x, *w, stream=handle), bitopt.mx_linear_grad_input(gate, *w, 130, stream=handle),
+               bitopt.mx_linear_grad_weight(gate, *q, 130, stream=handle),
+               bitopt.mx_matmul(*q, *w, 130, "e4m3", stream=handle), bitopt.mx_dequantize(*q, 130, "e4m3", stream=handle),
+               bitopt.swiglu_save8(gate, gate, stream=handle)[0]]
+        codes = bitopt.mx_quantize(x, "e4m3", stream=handle)
+        assert torch.cuda.current_stream() == other
+    torch.cuda.synchronize()
+    assert seen == [own.cuda_stream] * 7
+    for a, b in zip(got + list(codes), want + list(q)):
+        assert torch.equal(a, b)
+    # the calls beside them take the same object
+    monkeypatch.undo()
+    flat, qmap = x.view(-1), bitopt.create_dynamic_map(True).cuda()
+    want = bitopt.quantize_blockwise(flat, qmap)
+    codes, absmax = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    torch.cuda.synchronize()
+    bitopt.quantize_blockwise(flat, qmap, codes=codes, absmax=absmax, stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(codes, want[0]) and torch.equal(absmax, want[1])
