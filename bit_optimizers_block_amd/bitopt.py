@@ -563,6 +563,11 @@ def step_multi(hp, step, tensors, qmap1=None, qmap2=None, workspace=None, stream
 # These calls run once per layer and token, so a call on the current device and stream
 # takes the short way: each argument is looked at once, and the stream's handle is read
 # without building a stream object.
+#
+# They record nothing for automatic differentiation, whether or not an argument requires a
+# gradient: results are new tensors without a history (or the caller's own).  Gradients come
+# from the calls for them, mx_linear_grad_input, mx_linear_grad_weight and swiglu_backward8,
+# which a torch.autograd.Function of the caller's may wrap; quantization has none.
 
 MX_FORMATS = {"e2m1": 0, "e4m3": 1}
 

@@ -119,3 +119,32 @@ def test_streams_of_other_libraries(monkeypatch, given):
     bitopt.quantize_blockwise(flat, qmap, codes=codes, absmax=absmax, stream=handle)
     torch.cuda.synchronize()
     assert torch.equal(codes, want[0]) and torch.equal(absmax, want[1])
+
+
+def test_results_have_no_history():
+    """Arguments that require a gradient are taken, and their results require none."""
+    master = torch.nn.Parameter(values(1, 90, 130, "f32"))
+    x, dy = values(2, 5, 130, "bf16").requires_grad_(), values(3, 5, 90, "bf16")
+    w, q = bitopt.mx_quantize(master), bitopt.mx_quantize(x, "e4m3")
+    y = bitopt.mx_linear(x, *w)
+    s, saved = bitopt.swiglu_save8(x, x)
+    for t in (y, s, bitopt.mx_linear_grad_input(dy, *w, 130), bitopt.mx_linear_grad_weight(dy, *q, 130),
+              *bitopt.swiglu_backward8(s, saved), bitopt.mx_dequantize(*w, 130)):
+        assert not t.requires_grad and t.grad_fn is None
+
+    class Linear(torch.autograd.Function):
+        """The layer for automatic differentiation, made of the calls."""
+
+        @staticmethod
+        def forward(ctx, x, weight):
+            ctx.w, ctx.x, ctx.k = bitopt.mx_quantize(weight), bitopt.mx_quantize(x, "e4m3"), x.shape[1]
+            return bitopt.mx_linear(x, *ctx.w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return (bitopt.mx_linear_grad_input(dy, *ctx.w, ctx.k), bitopt.mx_linear_grad_weight(dy, *ctx.x, ctx.k))
+
+    got = Linear.apply(x, master)
+    got.backward(dy)
+    assert torch.equal(got, y) and torch.equal(x.grad, bitopt.mx_linear_grad_input(dy, *w, 130))
+    assert torch.equal(master.grad, bitopt.mx_linear_grad_weight(dy, *q, 130))
