@@ -249,8 +249,8 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // Bound: no unit alone.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and
 // 32 KB of writes through LDS per 32 contraction elements, against 1024 cycles of products;
-// counters show the matrix pipes busy 48% of the cycles and LDS 32%, the rest is waits that two
-// waves a SIMD do not fill.  Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 203 us
+// counters show the matrix pipes busy 51% of the cycles and LDS 34% (57% in the gradients, whose
+// transpose reads conflict on banks), the rest is waits that two waves a SIMD do not fill.  Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 203 us
 // (1350 TFLOP/s), weight grad 215 us, forward 212 us; E4M3: 209, 208 and 221.  Writing the next
 // stage after the products instead, in an earlier form: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter less, leave one wave a SIMD
 // and too few registers: 360, 499, 322.
@@ -380,17 +380,18 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemm
 // pattern, 64 separate dwords an instruction, scales were two thirds of the cache's
 // accesses: 8192 x 8192 x 8192 took 347 us.)
 //
-// Measured: 8192 x 8192 x 8192 265 us (4150 TFLOP/s), 8192 x 8192 x 2048 98 us, of which the
+// Measured: 8192 x 8192 x 8192 262 us (4200 TFLOP/s), 8192 x 8192 x 2048 87 to 98 us, of which the
 // results' stores are 16 and the steps 55: with one workgroup a CU, each of the four rounds of
 // tiles begins with empty buffers and ends in 128 KB of results that nothing overlaps.  The
 // matrix instructions alone reach 9500 TFLOP/s on zeros and 7000 on random codes, where the
-// card's power sets the clock; here their pipes are busy 47% of the cycles, LDS 27%, and the larger
+// card's power sets the clock; here their pipes are busy 44 to 47% of the cycles, LDS 25 to 27%, and the larger
 // size takes 230 us on zeros and 233 with the loads left out.  Four waves of 128 x 128 that
 // read a step's fragments under the one before took 266 and 110 us; eight such waves spill.
 // Reads and products of a SIMD's two waves in alternate phases, with a barrier after each: 265
 // and 100 (1024 x 4096 x 4096 16 -> 18).  One resident grid with the next tile's loads ahead of
-// the last one's stores took 154 us at the second size, non-temporal stores 138 (against 116 at
-// the time).
+// the last one's stores took 154 us at the second size, non-temporal stores 138, against 116 at
+// the time: both on earlier forms, of which the first spilled.  This one holds 208 registers of
+// 256, and neither has been tried on it.
 
 constexpr int kGemm4K = 128;
 
@@ -534,11 +535,21 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm4(MxGemmA
 
 // ------------------------------------------------------------------------ tile choice
 
-// Launches `big` (256 x 256 tiles), `mid` (128 x 128) or `small` (64 x 64): the largest
-// tile whose grid still occupies most of the 256 CUs.  Forward product, E2M1, us with big,
-// mid and small tiles at M x N x K (big tiles, mid tiles): 3584 x 3584 x 2048 (196, 784) 57,
-// 72, 88; 4096 x 2048 x 8192 (128, 512) 195, 159, 225; 1792 x 1792 x 2048 (49, 196) 54, 24,
-// 30; 2048 x 1024 x 2048 (32, 128) 52, 23, 19.
+// Launches `big` (256 x 256 tiles), `mid` (128 x 128) or `small` (64 x 64): the largest tile of
+// which there are enough for most of the 256 CUs; without enough of any, the smallest.  us with
+// big, mid and small tiles (E2M1; weight gradient E4M3):
+//   M x N (big tiles, mid tiles)   forward, K          input grad     weight grad    E2M1 x E2M1
+//   3584 x 3584 (196, 784)         55, 69, 84  2048                                  25, 26, 29
+//   3328 x 4096 (208, 832)         54, 67, 82  2048    57, 69, 96     60, 83, 105    23, 25, 29
+//   4096 x 2816 (176, 704)         99, 99, 141  4096   60, 55, 77     61, 65, 86     37, 35, 44
+//   4096 x 2048 (128, 512)         179, 135, 215  8192 60, 39, 56     61, 46, 64     65, 44, 64
+//   1792 x 1792 (49, 196)          50, 22, 30  2048    55, 23, 31     58, 28, 37     20, 9.6, 10
+//   2048 x 1280 (40, 160)          91, 39, 44  4096    55, 23, 25     58, 27, 30     32, 14.4, 13.5
+//   2048 x 1152 (40, 144)          91, 39, 44  4096    65, 22, 25     76, 27, 30     32, 14.0, 13.0
+//   2048 x 1024 (32, 128)          49, 21, 19  2048    55, 22, 19     57, 26, 22     19, 8.9, 7.1
+// (the gradients over 2048).  It does not look at how full the last round of tiles is: 4096 x 4608
+// (288, 1152), whose second round holds 32 big tiles, takes 107, 86 and 121 over 2048; and at 144
+// mid tiles small ones are taken, 12% slower but for two E2M1 operands.
 template <class Big, class Mid, class Small>
 hipError_t mx_by_tile(const MxGemmArgs& g, Big big, Mid mid, Small small) {
     auto tiles = [&](int t) { return ((int64_t)g.M + t - 1) / t * (((int64_t)g.N + t - 1) / t); };

@@ -16,8 +16,10 @@
 // leaves groups 1 and 2 with each other's elements, so the other operand follows).
 //
 // Measured, bf16 A, E2M1 B: one row against 50257 x 2048 (55 MB of codes and scales) 16.3 us,
-// two E2M1 operands 12.9 us, of which a launch is 2.6; 64 rows against 8192 x 8192 39 us,
-// bound by A's rows, which every workgroup reads from the caches.
+// two E2M1 operands 12.9 us, of which a launch is 2.6 (E4M3 B 24.2 us); 64 rows against
+// 8192 x 8192 38 us (E4M3 B 42.5), 17 rows against 4093 x 1999 8.5.  Those wait for one unit's loads
+// after the other with two waves a SIMD; A in E4M3, half the bytes, takes 32 and 5.7, so its
+// rows, which every workgroup reads from the caches, are not all of it.
 #include <algorithm>
 #include <type_traits>
 

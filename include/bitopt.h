@@ -583,7 +583,8 @@ BITOPT_API int bitopt_mx_linear_grad_weight(const void* dy, int32_t dtype, int64
  * 32: with s = 1 / (1 + exp(-gate)),
  *   forward    y = gate * s * up, and the codes and scales of gate and up
  *   backward   dgate = dy * up * s * (1 + gate * (1 - s)),  dup = dy * gate * s
- * with gate and up the values their codes stand for.  Arithmetic in fp32, rounded once.
+ * with gate and up the values their codes stand for.  Arithmetic in fp32, rounded once; s
+ * below 2^-126 (gate below some -87) counts as zero.
  */
 BITOPT_API int bitopt_swiglu_forward_mx8(const void* gate, const void* up, int32_t dtype, int64_t rows, int64_t cols,
                                          int64_t ldg, int64_t ldu, void* y, int64_t ldy, uint8_t* gate_codes,
