@@ -186,7 +186,8 @@ template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_mx_dequ
 
 // 1 / (1 + exp(-g)): 0 and 1 at the infinities.  fp32 results take the library's expf;
 // for 16-bit ones exp2 of the rounded product (relative error |g| 2^-24, against half a
-// step of 2^-9 or 2^-12) costs a fifth of it.
+// step of 2^-9 or 2^-12) costs a fifth of it.  The reciprocal gives zero for results below
+// 2^-126 (g below -87.34): what is lost is below |g| 2^-126 times the other factor.
 template <int DT> __device__ __forceinline__ float sigmoid(float g) {
     const float e = DT == kF32 ? expf(-g) : __builtin_amdgcn_exp2f(-1.44269504088896341f * g);
     return __builtin_amdgcn_rcpf(1.0f + e);

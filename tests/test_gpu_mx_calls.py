@@ -148,3 +148,22 @@ def test_results_have_no_history():
     got.backward(dy)
     assert torch.equal(got, y) and torch.equal(x.grad, bitopt.mx_linear_grad_input(dy, *w, 130))
     assert torch.equal(master.grad, bitopt.mx_linear_grad_weight(dy, *q, 130))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_gates_far_below_zero(dtype):
+    """A sigmoid below 2^-126 counts as zero; down to there it is as exact as elsewhere."""
+    big = 2.0**14 if dtype == "f16" else 2.0**100
+    gate = torch.tensor([[-80.0, -86.0, -87.0, -87.5, -88.5, -95.0, -104.0, -1000.0]], device="cuda").to(DT[dtype])
+    up = torch.full_like(gate, big)
+    y, saved = bitopt.swiglu_save8(gate, up)
+    exact = (gate.double() * torch.sigmoid(gate.double()) * big)[0]
+    half = torch.finfo(DT[dtype]).eps / 2
+    # the exponential's argument is off by |g| 2^-24, then a few roundings: (|g| + 8) 2^-23; and
+    # half of fp16's smallest step
+    limit = exact.abs() * ((gate.double()[0].abs() + 8) * 2.0**-23 + half) + (2.0**-25 if dtype == "f16" else 0)
+    assert ((y[0].double() - exact).abs()[:3] <= limit[:3]).all()
+    assert (y[0, 3:] == 0).all()
+    dgate, dup = bitopt.swiglu_backward8(torch.ones_like(up), saved)    # dy up has to be finite
+    codes = bitopt.mx_dequantize(saved[0], saved[1], 8, "e4m3")[0]
+    assert (dgate[0, codes < -87.34] == 0).all() and (dup[0, codes < -87.34] == 0).all()
