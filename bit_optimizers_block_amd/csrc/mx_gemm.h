@@ -250,10 +250,11 @@ __device__ __forceinline__ void lds_barrier() {
 // Bound: no unit alone.  A 256 x 256 tile on eight waves of 128 x 64 moves 96 KB of fragments and
 // 32 KB of writes through LDS per 32 contraction elements, against 1024 cycles of products;
 // counters show the matrix pipes busy 51% of the cycles and LDS 34% (57% in the gradients, whose
-// transpose reads conflict on banks), the rest is waits that two waves a SIMD do not fill.  Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 203 us
-// (1350 TFLOP/s), weight grad 215 us, forward 212 us; E4M3: 209, 208 and 221.  Writing the next
-// stage after the products instead, in an earlier form: 304, 316, 314.  Four waves of 128 x 128, whose LDS traffic is a quarter less, leave one wave a SIMD
-// and too few registers: 360, 499, 322.
+// transpose reads conflict on banks), the rest is waits that two waves a SIMD do not fill.
+// Measured at 8192 x 8192 x 2048, bf16 and E2M1: input grad 203 us (1350 TFLOP/s), weight grad
+// 215 us, forward 212 us; E4M3: 209, 208 and 221.  Earlier forms: the next stage written after the
+// products 304, 316, 314; four waves of 128 x 128, whose LDS traffic is a quarter less, which leave
+// one wave a SIMD and too few registers, 360, 499, 322.
 template <int DT, int ASRC, int BSRC, int BM, int BN, int WM, int WN, bool WHOLE>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_mx_gemm16(MxGemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
