@@ -226,8 +226,8 @@ __device__ __forceinline__ f32x4 mfma_e2m1_at(u32x4 a, u32x4 b, f32x4 c, uint32_
 }
 
 // Four consecutive output elements of a row, columns n .. n+3 (those below N), with the
-// old values added first when `accumulate`.
-__device__ __forceinline__ void mx_store4(const MxGemmArgs& g, int64_t m, int n, f32x4 v) {
+// old values added first when `accumulate`.  Args has out, ldo, out_dtype, accumulate, M and N.
+template <class Args> __device__ __forceinline__ void mx_store4(const Args& g, int64_t m, int n, f32x4 v) {
     const int64_t e = m * g.ldo + n;
     const bool whole = n + 4 <= g.N;
     if (g.out_dtype == kF32) {
@@ -263,7 +263,8 @@ __device__ __forceinline__ void mx_store4(const MxGemmArgs& g, int64_t m, int n,
 // Two neighbouring 16 x 16 result tiles of row m, columns n .. n+31: lane group q holds
 // columns 4 q .. + 3 of both.  16-bit results are exchanged between neighbouring groups
 // first, so a lane stores eight consecutive columns and a row gets whole 64-byte segments.
-__device__ __forceinline__ void mx_store_pair(const MxGemmArgs& g, int64_t m, int n, int q, f32x4 v, f32x4 w) {
+template <class Args>
+__device__ __forceinline__ void mx_store_pair(const Args& g, int64_t m, int n, int q, f32x4 v, f32x4 w) {
     if (g.out_dtype == kF32 || g.accumulate || n + 32 > g.N) {
         if (m >= g.M) return;
         if (n + 4 * q < g.N) mx_store4(g, m, n + 4 * q, v);

@@ -10,81 +10,10 @@
 // 84.  dequantize streams its result (E2M1 68 -> 52).  quantize reads what was just computed:
 // its loads keep the caches (streaming: 60 -> 58 from HBM, but 8.3 -> 9.2 where 8192 x 2048
 // still lies in the Infinity Cache), and so do codes, which the next call reads.
-#include <algorithm>
-
 #include "launch.h"
-#include "mx.h"
+#include "mx_rows.h"
 
 namespace bitopt {
-
-// Lanes along a row: 2^lanes_log2 of a workgroup's 256, the rest of the workgroup takes
-// further rows; `steps` row groups per workgroup.
-struct RowGrid {
-    int32_t lanes_log2, chunks, steps;
-};
-
-constexpr int kRowSteps = 4;
-
-static RowGrid row_grid(int64_t rows, int64_t cols, int per_lane, dim3& grid) {
-    RowGrid g{};
-    const int64_t items = mx_padded(cols) / per_lane;
-    g.lanes_log2 = 4;
-    while (g.lanes_log2 < 8 && (int64_t{1} << g.lanes_log2) < items) ++g.lanes_log2;
-    g.chunks = (int32_t)((items + (int64_t{1} << g.lanes_log2) - 1) >> g.lanes_log2);
-    const int64_t per = kThreads >> g.lanes_log2;
-    const int64_t groups = (rows + per - 1) / per;
-    g.steps = groups * g.chunks >= 4096 ? kRowSteps : 1;
-    grid = dim3((unsigned)g.chunks, (unsigned)std::min<int64_t>((groups + g.steps - 1) / g.steps, 65535));
-    return g;
-}
-
-// Elements per lane.
-template <int DT> constexpr int kPer = DT == kF32 ? 4 : 8;
-
-// One item of a row as fp32, from any address aligned to the element; zeros from element n on.
-// before: elements of the row ahead of it.
-template <int DT, bool NT> __device__ __forceinline__ void ld_item(const void* base, int64_t e, int n, int64_t before,
-                                                                         float v[kPer<DT>]) {
-    if constexpr (DT == kF32) {
-        const float* p = reinterpret_cast<const float*>(base) + e;
-        if (n >= 4) {
-            const f32x4 a = ld16_a4<NT>(p);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = a[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = j < n ? gbl(p)[j] : 0.0f;
-        }
-    } else {
-        const u32x4 r = ld_half8<NT>(reinterpret_cast<const uint16_t*>(base) + e, n, before);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = widen<DT>(r[j / 2] >> (16 * (j & 1)));
-    }
-}
-
-template <int DT> __device__ __forceinline__ void st_item(void* base, int64_t e, int n, const float v[kPer<DT>]) {
-    if constexpr (DT == kF32) {
-        float* p = reinterpret_cast<float*>(base) + e;
-        if (n >= 4) {
-            st16_a4<true>(p, f32x4{v[0], v[1], v[2], v[3]});
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < n) gbl(p)[j] = v[j];
-        }
-    } else {
-        uint16_t* p = reinterpret_cast<uint16_t*>(base) + e;
-        const u32x4 r = {narrow2<DT>(v[0], v[1]), narrow2<DT>(v[2], v[3]), narrow2<DT>(v[4], v[5]),
-                         narrow2<DT>(v[6], v[7])};
-        if (n >= 8) {
-            st16_a2<true>(p, r);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) gbl(p)[j] = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
-        }
-    }
-}
 
 // Codes of this lane's item: bytes per item, and the type that holds them.
 template <int DT, int FMT> constexpr int kCodeBytes = FMT == kMxE2M1 ? kPer<DT> / 2 : kPer<DT>;
@@ -142,26 +71,6 @@ __device__ __forceinline__ void ld_codes(const uint8_t* codes, const uint8_t* sc
         else if constexpr (kPer<DT> == 4) mx_decode4_e4m3((uint32_t)w, s, v);
         else mx_decode4_e4m3(w[h], s, v + 4 * h);
     }
-}
-
-// Runs f(row, item) for every item of the padded rows.  The lanes of a block are in or out
-// together (items per row is a multiple of 16).
-template <class F> __device__ __forceinline__ void for_items(const RowGrid& g, int64_t rows, int32_t items, F f) {
-    const int lanes = 1 << g.lanes_log2;
-    const int32_t item = (int32_t)blockIdx.x * lanes + ((int)threadIdx.x & (lanes - 1));
-    const int64_t per = kThreads >> g.lanes_log2;
-    if (item >= items) return;
-    const int64_t stride = per * gridDim.y;
-    int64_t row = per * blockIdx.y + (threadIdx.x >> g.lanes_log2);
-    for (; row + (kRowSteps - 1) * stride < rows; row += kRowSteps * stride) {
-#pragma unroll
-        for (int s = 0; s < kRowSteps; ++s) f(row + s * stride, item);
-    }
-    for (; row < rows; row += stride) f(row, item);
-}
-
-template <int DT> __device__ __forceinline__ int item_elems(int64_t cols, int32_t item) {
-    return (int)max((int64_t)0, min((int64_t)kPer<DT>, cols - kPer<DT> * (int64_t)item));
 }
 
 template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_mx_quantize(MxCodecArgs a, RowGrid g) {
@@ -241,7 +150,7 @@ template <int DT> __global__ __launch_bounds__(kThreads) void k_swiglu_backward(
 #define BITOPT_MX_LAUNCH(kernel, args)                                              \
     do {                                                                            \
         dim3 grid;                                                                  \
-        const RowGrid g = row_grid((args).rows, (args).cols, dtype == kF32 ? 4 : 8, grid);                 \
+        const RowGrid g = row_grid((args).rows, mx_padded((args).cols) / (dtype == kF32 ? 4 : 8), grid); \
         hipLaunchKernelGGL(HIP_KERNEL_NAME(kernel), grid, dim3(kThreads), 0, s, args, g); \
         return hipGetLastError();                                                   \
     } while (0)

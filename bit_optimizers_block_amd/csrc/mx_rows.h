@@ -1,0 +1,113 @@
+// mx_rows.h -- kernels that go over the rows of a matrix once: the grid, and loads and stores
+// of a lane's 16 bytes of a row from any address aligned to the element.
+#pragma once
+
+#include <algorithm>
+
+#include "mx.h"
+
+namespace bitopt {
+
+// Lanes along a row: 2^lanes_log2 of a workgroup's 256, the rest of the workgroup takes
+// further rows; `steps` row groups per workgroup.
+struct RowGrid {
+    int32_t lanes_log2, chunks, steps;
+};
+
+constexpr int kRowSteps = 4;
+
+inline RowGrid row_grid(int64_t rows, int64_t items, dim3& grid) {
+    RowGrid g{};
+    g.lanes_log2 = 4;
+    while (g.lanes_log2 < 8 && (int64_t{1} << g.lanes_log2) < items) ++g.lanes_log2;
+    g.chunks = (int32_t)((items + (int64_t{1} << g.lanes_log2) - 1) >> g.lanes_log2);
+    const int64_t per = kThreads >> g.lanes_log2;
+    const int64_t groups = (rows + per - 1) / per;
+    g.steps = groups * g.chunks >= 4096 ? kRowSteps : 1;
+    grid = dim3((unsigned)g.chunks, (unsigned)std::min<int64_t>((groups + g.steps - 1) / g.steps, 65535));
+    return g;
+}
+
+#ifdef __HIPCC__
+
+// Elements per lane.
+template <int DT> constexpr int kPer = DT == kF32 ? 4 : 8;
+
+// One item of a row as fp32, from any address aligned to the element; zeros from element n on.
+// before: elements of the row ahead of it.
+template <int DT, bool NT> __device__ __forceinline__ void ld_item(const void* base, int64_t e, int n, int64_t before,
+                                                                         float v[kPer<DT>]) {
+    if constexpr (DT == kF32) {
+        const float* p = reinterpret_cast<const float*>(base) + e;
+        if (n >= 4) {
+            const f32x4 a = ld16_a4<NT>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = a[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = j < n ? gbl(p)[j] : 0.0f;
+        }
+    } else {
+        const u32x4 r = ld_half8<NT>(reinterpret_cast<const uint16_t*>(base) + e, n, before);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = widen<DT>(r[j / 2] >> (16 * (j & 1)));
+    }
+}
+
+template <int DT> __device__ __forceinline__ void st_item(void* base, int64_t e, int n, const float v[kPer<DT>]) {
+    if constexpr (DT == kF32) {
+        float* p = reinterpret_cast<float*>(base) + e;
+        if (n >= 4) {
+            st16_a4<true>(p, f32x4{v[0], v[1], v[2], v[3]});
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) gbl(p)[j] = v[j];
+        }
+    } else {
+        uint16_t* p = reinterpret_cast<uint16_t*>(base) + e;
+        const u32x4 r = {narrow2<DT>(v[0], v[1]), narrow2<DT>(v[2], v[3]), narrow2<DT>(v[4], v[5]),
+                         narrow2<DT>(v[6], v[7])};
+        if (n >= 8) {
+            st16_a2<true>(p, r);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) gbl(p)[j] = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
+
+// Eight elements of a row whatever the type: as ld_item and st_item, fp32 in two of theirs.
+template <int DT, bool NT> __device__ __forceinline__ void ld_eight(const void* base, int64_t e, int n, int64_t before, float v[8]) {
+    ld_item<DT, NT>(base, e, n, before, v);
+    if constexpr (DT == kF32) ld_item<DT, NT>(base, e + 4, n - 4, before + 4, v + 4);
+}
+template <int DT> __device__ __forceinline__ void st_eight(void* base, int64_t e, int n, const float v[8]) {
+    st_item<DT>(base, e, n, v);
+    if constexpr (DT == kF32) st_item<DT>(base, e + 4, n - 4, v + 4);
+}
+
+// Runs f(row, item) for every item of the rows.  Where a row has a multiple of 16 items, the
+// lanes of an aligned group of 16 are in or out together.
+template <class F> __device__ __forceinline__ void for_items(const RowGrid& g, int64_t rows, int32_t items, F f) {
+    const int lanes = 1 << g.lanes_log2;
+    const int32_t item = (int32_t)blockIdx.x * lanes + ((int)threadIdx.x & (lanes - 1));
+    const int64_t per = kThreads >> g.lanes_log2;
+    if (item >= items) return;
+    const int64_t stride = per * gridDim.y;
+    int64_t row = per * blockIdx.y + (threadIdx.x >> g.lanes_log2);
+    for (; row + (kRowSteps - 1) * stride < rows; row += kRowSteps * stride) {
+#pragma unroll
+        for (int s = 0; s < kRowSteps; ++s) f(row + s * stride, item);
+    }
+    for (; row < rows; row += stride) f(row, item);
+}
+
+template <int DT> __device__ __forceinline__ int item_elems(int64_t cols, int32_t item) {
+    return (int)max((int64_t)0, min((int64_t)kPer<DT>, cols - kPer<DT> * (int64_t)item));
+}
+
+#endif  // __HIPCC__
+
+}  // namespace bitopt
