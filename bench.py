@@ -477,13 +477,13 @@ def cpu_baseline_multi(wl, target_s=15.0):
 
 
 def source_hash() -> str:
-    """Hash of the sources of the optimizer step and its codec (the MX operators, mx*, are not
-    among the workloads): HBM traffic counted by the profiler is reported only while the
+    """Hash of the sources of the optimizer step and its codec (the MX, F8 and layer operators
+    are not among the workloads): HBM traffic counted by the profiler is reported only while the
     kernels are unchanged since the counters were taken."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "bit_optimizers_block_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.startswith("mx"):
+        if f.startswith(("mx", "f8", "layer")):
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())

@@ -145,6 +145,11 @@ def lib():
                                              ctypes.c_int),
             "bitopt_swiglu_forward_mx8": ([P, P, i32, i64, i64, i64, i64, P, i64, P, P, P, P, P], ctypes.c_int),
             "bitopt_swiglu_backward_mx8": ([P, i32, i64, i64, i64, P, P, P, P, P, i64, P, i64, P], ctypes.c_int),
+            "bitopt_f8_code_bytes": ([i64], i64),
+            "bitopt_f8_scale_count": ([i64, i64, i32], i64),
+            "bitopt_f8_quantize": ([P, i32, i64, i64, i64, i32, i32, P, P, P, P, P], ctypes.c_int),
+            "bitopt_f8_dequantize": ([P, P, i32, i32, i64, i64, P, i32, i64, P], ctypes.c_int),
+            "bitopt_f8_matmul": ([P, P, i32, P, P, i32, i32, i64, i64, i64, P, i32, i64, i32, P], ctypes.c_int),
             "bitopt_step_multi_planned_dscalars": ([ctypes.POINTER(MultiPlanC), HP, P, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
@@ -815,3 +820,131 @@ def swiglu_backward8(dy, saved, dgate=None, dup=None, stream=None):
                                             uc.data_ptr(), us.data_ptr(), dgate.data_ptr(), lddg, dup.data_ptr(), lddu,
                                             _current(device)))
     return dgate, dup
+
+
+# ------------------------------------------------------------------- F8 matrices
+#
+# As the MX calls: each argument is looked at once, nothing is recorded for automatic
+# differentiation, and a call on the current device and stream takes the short way.
+
+F8_FORMATS = {"e4m3": 0, "e5m2": 1}
+F8_BLOCKS = {"rows": 0, "tiles": 1}
+
+
+def f8_code_bytes(cols: int) -> int:
+    """Bytes of codes in one row of an F8 matrix: rows are padded to 128 elements."""
+    return (cols + 127) // 128 * 128
+
+
+def f8_scale_shape(rows: int, cols: int, blocks: str = "rows"):
+    """Shape of an F8 matrix's scales: (blocks of a row, rows), or tiles as they lie."""
+    return (-(-rows // 128), -(-cols // 128)) if _f8_blocks(blocks) else (-(-cols // 128), rows)
+
+
+def _f8_format(fmt):
+    f = F8_FORMATS.get(fmt)
+    if f is None:
+        raise ValueError(f"unknown F8 format {fmt!r} (one of {sorted(F8_FORMATS)})")
+    return f
+
+
+def _f8_blocks(blocks):
+    b = F8_BLOCKS.get(blocks)
+    if b is None:
+        raise ValueError(f"unknown F8 blocks {blocks!r} (one of {sorted(F8_BLOCKS)})")
+    return b
+
+
+def _f8_operand(codes, scales, cols, blocks, name, device):
+    """Checks an F8 matrix of `cols` columns; returns its rows."""
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
+        raise TypeError(f"{name}: expected torch.uint8 codes and torch.float32 scales, got {codes.dtype}, {scales.dtype}")
+    kb = (cols + 127) // 128
+    rows = codes.size(0) if codes.dim() == 2 else -1
+    if codes.shape != (rows, kb * 128) or not codes.is_contiguous():
+        raise ValueError(f"{name} codes: expected a contiguous matrix of {kb * 128} bytes a row for {cols} columns, got "
+                         f"shape {tuple(codes.shape)}")
+    shape = ((rows + 127) // 128, kb) if blocks else (kb, rows)
+    if scales.shape != shape or not scales.is_contiguous():
+        raise ValueError(f"{name} scales: expected a contiguous matrix of shape {shape} for {rows} x {cols} elements, got "
+                         f"{tuple(scales.shape)}")
+    if not codes.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if codes.device != device or scales.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return rows
+
+
+def _f8_new(rows, cols, blocks, device):
+    kb = (cols + 127) // 128
+    shape = ((rows + 127) // 128, kb) if blocks else (kb, rows)
+    return (torch.empty_strided((rows, kb * 128), (kb * 128, 1), dtype=torch.uint8, device=device),
+            torch.empty_strided(shape, (shape[1], 1), dtype=torch.float32, device=device))
+
+
+def f8_quantize(x, fmt: str = "e4m3", blocks: str = "rows", give: str = "rows", out=None, stream=None):
+    """The F8 form of a matrix: (codes, scales).  give="columns": that of its transpose, with
+    blocks along x's columns; "both": (codes, scales, codes_t, scales_t) from one reading.
+    out: the caller's tensors for the result, in that order."""
+    rows, cols, ldx = _rows(x, "x")
+    dt, device = _dt(x), x.device
+    f, b = _f8_format(fmt), _f8_blocks(blocks)
+    if give not in ("rows", "columns", "both"):
+        raise ValueError(f"give must be 'rows', 'columns' or 'both', got {give!r}")
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return f8_quantize(x, fmt, blocks, give, out)
+    if out is None:
+        out = () if give == "columns" else _f8_new(rows, cols, b, device)
+        if give != "rows":
+            out += _f8_new(cols, rows, b, device)
+    else:
+        out = tuple(out)
+        if len(out) != (4 if give == "both" else 2):
+            raise ValueError(f"out: expected {4 if give == 'both' else 2} tensors, got {len(out)}")
+        if give != "columns" and _f8_operand(*out[:2], cols, b, "the result", device) != rows:
+            raise ValueError(f"the result: expected {rows} rows of codes, got {out[0].size(0)}")
+        if give != "rows" and _f8_operand(*out[-2:], rows, b, "the transposed result", device) != cols:
+            raise ValueError(f"the transposed result: expected {cols} rows of codes, got {out[-2].size(0)}")
+    p = [t.data_ptr() for t in out]
+    c, s = (None, None) if give == "columns" else p[:2]
+    ct, st = (None, None) if give == "rows" else p[-2:]
+    _check(lib().bitopt_f8_quantize(x.data_ptr(), dt, rows, cols, ldx, f, b, c, s, ct, st, _current(device)))
+    return out
+
+
+def f8_dequantize(codes, scales, cols: int, fmt: str = "e4m3", blocks: str = "rows", out=None, dtype=torch.float32,
+                  stream=None):
+    """The values of an F8 matrix of `cols` columns."""
+    device = codes.device
+    f, b = _f8_format(fmt), _f8_blocks(blocks)
+    rows = _f8_operand(codes, scales, cols, b, "the input", device)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return f8_dequantize(codes, scales, cols, fmt, blocks, out, dtype)
+    out, ldo = _mx_result(out, rows, cols, dtype, device, "out")
+    _check(lib().bitopt_f8_dequantize(codes.data_ptr(), scales.data_ptr(), f, b, rows, cols, out.data_ptr(), _dt(out),
+                                      ldo, _current(device)))
+    return out
+
+
+def f8_matmul(a_codes, a_scales, b_codes, b_scales, k: int, a_fmt: str = "e4m3", b_fmt: str = "e4m3",
+              b_blocks: str = "rows", out=None, dtype=torch.bfloat16, accumulate: bool = False, stream=None):
+    """a b^T for F8 matrices a (m x k, by rows) and b (n x k, by rows or tiles); `accumulate`
+    adds it to `out`."""
+    device = a_codes.device
+    fa, fb, b = _f8_format(a_fmt), _f8_format(b_fmt), _f8_blocks(b_blocks)
+    m = _f8_operand(a_codes, a_scales, k, 0, "a", device)
+    n = _f8_operand(b_codes, b_scales, k, b, "b", device)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return f8_matmul(a_codes, a_scales, b_codes, b_scales, k, a_fmt, b_fmt, b_blocks, out, dtype, accumulate)
+    out, ldo = _mx_result(out, m, n, dtype, device, "out")
+    _check(lib().bitopt_f8_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(), b_scales.data_ptr(), fb,
+                                  b, m, n, k, out.data_ptr(), _dt(out), ldo, 1 if accumulate else 0, _current(device)))
+    return out

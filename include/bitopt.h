@@ -594,6 +594,74 @@ BITOPT_API int bitopt_swiglu_backward_mx8(const void* dy, int32_t dtype, int64_t
                                           const uint8_t* up_codes, const uint8_t* up_scales, void* dgate, int64_t lddg,
                                           void* dup, int64_t lddu, void* stream);
 
+/* ---------------------------------------------------------------- F8 matrices
+ *
+ * 8-bit floating-point matrices with an fp32 scale for each block of 128: operands of a
+ * product that runs on the 8-bit matrix instructions, for weights, activations and the
+ * gradients between layers.  A matrix of rows x cols values is held as
+ *   codes    rows x bitopt_f8_code_bytes(cols) bytes, rows padded to 128 with zero codes
+ *   scales   bitopt_f8_scale_count(rows, cols, blocks) floats
+ * both aligned to 16 bytes.
+ *   BITOPT_F8_ROWS    a block is 128 consecutive elements of a row; scales lie block by
+ *                     block: that of row r, block c at c * rows + r
+ *   BITOPT_F8_TILES   a block is a tile of 128 x 128; that of tile row r, tile column c at
+ *                     r * ceil(cols / 128) + c
+ *   BITOPT_F8_E4M3    as BITOPT_MX_E4M3's elements: largest 448, smallest 2^-9
+ *   BITOPT_F8_E5M2    sign, 5 exponent bits (bias 15), 2 fraction bits; largest 57344,
+ *                     smallest 2^-16; 0x7c and 0xfc are infinities, what is above them NaN
+ * An element is its code's value times its block's scale; any finite scale may stand there.
+ * The conventions of the MX calls hold here: sizes of zero and above 2^30, distances of
+ * rows, results that share memory, no workspace, graphs, the same bits on every run.
+ */
+#define BITOPT_F8_E4M3 0
+#define BITOPT_F8_E5M2 1
+#define BITOPT_F8_ROWS 0
+#define BITOPT_F8_TILES 1
+
+/* Bytes of codes in one row (-1: cols < 0 or above 2^30), and scales of a matrix (-1: the
+ * same, or unknown blocks). */
+BITOPT_API int64_t bitopt_f8_code_bytes(int64_t cols);
+BITOPT_API int64_t bitopt_f8_scale_count(int64_t rows, int64_t cols, int32_t blocks);
+
+/*
+ * Quantization to F8.  With top the format's largest value and amax the block's largest |x|,
+ * at least top 2^-126: r = top / amax in fp32, its significand cut to 13 bits; codes are x r
+ * rounded to nearest, ties to the even code, signs kept (also of zero); the scale is 1 / r in
+ * fp32.  No element saturates.  A block that holds an infinity or a NaN gets the scale NaN
+ * and zero codes: all of it decodes to NaN.
+ *   codes, scales       the matrix, or both NULL
+ *   codes_t, scales_t   its transpose (cols x rows, blocks along the columns of x), or both
+ *                       NULL; of tiles, the transpose of the same codes
+ * Both are made from one reading of x: a forward product contracts along the rows, the
+ * gradient of its weights along the columns.
+ */
+BITOPT_API int bitopt_f8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                  int32_t format, int32_t blocks, uint8_t* codes, float* scales, uint8_t* codes_t,
+                                  float* scales_t, void* stream);
+
+/* out[r][c] = code's value * scale in fp32, then rounded to nearest-even into dtype. */
+BITOPT_API int bitopt_f8_dequantize(const uint8_t* codes, const float* scales, int32_t format, int32_t blocks,
+                                    int64_t rows, int64_t cols, void* out, int32_t dtype, int64_t ldo, void* stream);
+
+/*
+ * Product of two F8 matrices: out[m][n] = sum_k a[m][k] b[n][k], a m x k by rows, b n x k by
+ * rows or tiles; accumulate != 0 adds it to out.  Each block of 128 is summed by itself,
+ * multiplied by its scales and added in fp32; the result is rounded once into out_dtype.  The
+ * three products of a linear layer y = x W^T: x (rows) with W (tiles); dy (rows) with W^T
+ * (tiles); dy^T (rows) with x^T (rows).
+ * With a 16-bit result and more than 64 rows of a, a block's sum runs on the 8-bit matrix
+ * instruction, which aligns the products to the largest one and drops what lies some 17 bits
+ * below it; with an fp32 result, and for up to 64 rows, on decoded elements, where products
+ * are exact and sums are those of fp32.
+ * Up to 64 rows of a take a form that reads b once.  k above 2^24 gives UNSUPPORTED, and so
+ * do products that one launch does not hold: some 2^39 results, or 2^28 columns for up to
+ * 64 rows.
+ */
+BITOPT_API int bitopt_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t a_format,
+                                const uint8_t* b_codes, const float* b_scales, int32_t b_format, int32_t b_blocks,
+                                int64_t m, int64_t n, int64_t k, void* out, int32_t out_dtype, int64_t ldo,
+                                int32_t accumulate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
