@@ -101,6 +101,7 @@ def lib():
                               "or python bit_optimizers_block_amd/build.py")
         L = ctypes.CDLL(LIB_PATH)
         P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        u64, f32, f64 = ctypes.c_uint64, ctypes.c_float, ctypes.c_double
         HP = ctypes.POINTER(HParams)
         sigs = {
             "bitopt_last_error": ([], ctypes.c_char_p),
@@ -150,6 +151,13 @@ def lib():
             "bitopt_f8_quantize": ([P, i32, i64, i64, i64, i32, i32, P, P, P, P, P], ctypes.c_int),
             "bitopt_f8_dequantize": ([P, P, i32, i32, i64, i64, P, i32, i64, P], ctypes.c_int),
             "bitopt_f8_matmul": ([P, P, i32, P, P, i32, i32, i64, i64, i64, P, i32, i64, i32, P], ctypes.c_int),
+            "bitopt_dropout_forward": ([P, i32, i64, i64, i64, P, i64, f64, u64, u64, P, P, i64, P], ctypes.c_int),
+            "bitopt_dropout_backward": ([P, i32, i64, i64, i64, f64, u64, u64, P, P, i64, P], ctypes.c_int),
+            "bitopt_embedding_forward": ([P, i32, i64, P, i32, i64, i64, i64, f32, P, i32, i64, P], ctypes.c_int),
+            "bitopt_mx_embedding_forward": ([P, i32, i64, P, P, i32, i64, i64, f32, P, i32, i64, P], ctypes.c_int),
+            "bitopt_embedding_workspace_bytes": ([i64, i64, i64], i64),
+            "bitopt_embedding_backward": ([P, i32, i64, i64, i64, P, i32, i64, f32, P, i32, i64, i32, P, i64, P],
+                                          ctypes.c_int),
             "bitopt_step_multi_planned_dscalars": ([ctypes.POINTER(MultiPlanC), HP, P, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
@@ -947,4 +955,142 @@ def f8_matmul(a_codes, a_scales, b_codes, b_scales, k: int, a_fmt: str = "e4m3",
     out, ldo = _mx_result(out, m, n, dtype, device, "out")
     _check(lib().bitopt_f8_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(), b_scales.data_ptr(), fb,
                                   b, m, n, k, out.data_ptr(), _dt(out), ldo, 1 if accumulate else 0, _current(device)))
+    return out
+
+
+# ------------------------------------------------- dropout, embedding and its gradient
+#
+# As the MX calls: nothing is recorded for automatic differentiation; the gradients are the
+# calls dropout_backward and embedding_backward.
+
+TOKENS = {torch.int32: 0, torch.int64: 1}
+
+
+def _u64(v, name):
+    v = int(v)
+    if not 0 <= v < 2**64:
+        raise ValueError(f"{name} must lie in [0, 2^64), got {v}")
+    return v
+
+
+def _dropout(fn, x, p, seed, call, residual, out, counter, stream):
+    rows, cols, ldx = _rows(x, "x")
+    dt, device = _dt(x), x.device
+    seed, call = _u64(seed, "seed"), _u64(call, "call")
+    ldr = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("x and residual must have one shape and type")
+        ldr = _rows(residual, "residual", device)[2]
+    if counter is not None:
+        if counter.dtype is not torch.int64 or counter.numel() != 1:
+            raise TypeError(f"counter: expected one torch.int64, got {counter.numel()} {counter.dtype}")
+        if counter.device != device:
+            raise ValueError(f"counter must be on {device}")
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return _dropout(fn, x, p, seed, call, residual, out, counter, None)
+    out, ldo = _mx_result(out, rows, cols, x.dtype, device, "out")
+    if out.dtype != x.dtype:
+        raise TypeError(f"out: expected {x.dtype}, got {out.dtype}")
+    c = None if counter is None else counter.data_ptr()
+    if fn == "forward":
+        r = None if residual is None else residual.data_ptr()
+        _check(lib().bitopt_dropout_forward(x.data_ptr(), dt, rows, cols, ldx, r, ldr, p, seed, call, c, out.data_ptr(), ldo,
+                                            _current(device)))
+    else:
+        _check(lib().bitopt_dropout_backward(x.data_ptr(), dt, rows, cols, ldx, p, seed, call, c, out.data_ptr(), ldo,
+                                             _current(device)))
+    return out
+
+
+def dropout(x, p: float, seed: int, call: int = 0, residual=None, out=None, counter=None, stream=None):
+    """x with elements dropped with probability p (a multiple of 2^-16) and the others grown, added
+    to `residual` where given.  The mask follows from seed, call and an element's place: nothing is
+    kept for dropout_backward.  counter: a device int64 added to call when the kernel runs (for
+    captured graphs).  out may be x or residual."""
+    return _dropout("forward", x, p, seed, call, residual, out, counter, stream)
+
+
+def dropout_backward(dy, p: float, seed: int, call: int = 0, out=None, counter=None, stream=None):
+    """The gradient of dropout's x from dy, with the forward call's p, seed, call and counter.  out
+    may be dy."""
+    return _dropout("backward", dy, p, seed, call, None, out, counter, stream)
+
+
+def _tokens(tokens, device=None):
+    if tokens.dtype not in TOKENS:
+        raise TypeError(f"tokens: expected torch.int32 or torch.int64, got {tokens.dtype}")
+    if not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    if not tokens.is_cuda:
+        raise ValueError("tokens must be a device tensor")
+    if device is not None and tokens.device != device:
+        raise ValueError(f"tokens is on {tokens.device}, other arguments on {device}")
+    return TOKENS[tokens.dtype], tokens.numel()
+
+
+def embedding(tokens, table, scale: float = 1.0, out=None, dtype=None, stream=None):
+    """scale * table[token] for every token, in their order: a matrix of tokens.numel() rows; dtype
+    defaults to the table's.  A token outside the table (padding, say -1) gives zeros."""
+    vocab, width, ldt = _rows(table, "table")
+    dt, device = _dt(table), table.device
+    kind, count = _tokens(tokens, device)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return embedding(tokens, table, scale, out, dtype)
+    out, ldo = _mx_result(out, count, width, dtype or table.dtype, device, "out")
+    _check(lib().bitopt_embedding_forward(tokens.data_ptr(), kind, count, table.data_ptr(), dt, vocab, width, ldt, scale,
+                                          out.data_ptr(), _dt(out), ldo, _current(device)))
+    return out
+
+
+def mx_embedding(tokens, codes, scales, cols: int, fmt: str = "e2m1", scale: float = 1.0, out=None,
+                 dtype=torch.bfloat16, stream=None):
+    """embedding() from a table held as an MX matrix of `cols` columns, as mx_linear's weights."""
+    device = codes.device
+    f, vocab = _mx_operand(codes, scales, cols, fmt, "the table", device)
+    kind, count = _tokens(tokens, device)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return mx_embedding(tokens, codes, scales, cols, fmt, scale, out, dtype)
+    out, ldo = _mx_result(out, count, cols, dtype, device, "out")
+    _check(lib().bitopt_mx_embedding_forward(tokens.data_ptr(), kind, count, codes.data_ptr(), scales.data_ptr(), f, vocab,
+                                             cols, scale, out.data_ptr(), _dt(out), ldo, _current(device)))
+    return out
+
+
+def embedding_workspace_bytes(count: int, vocab: int, width: int) -> int:
+    return int(lib().bitopt_embedding_workspace_bytes(count, vocab, width))
+
+
+def embedding_backward(dy, tokens, vocab: int, scale: float = 1.0, out=None, dtype=torch.float32,
+                       accumulate: bool = False, workspace=None, stream=None):
+    """The gradient of embedding's table (vocab x width) from dy (one row a token); `accumulate`
+    adds it to `out`, touching only the rows of the batch's tokens.  workspace: a device uint8
+    tensor of embedding_workspace_bytes(); allocated if not given."""
+    count, width, lddy = _rows(dy, "dy")
+    dt, device = _dt(dy), dy.device
+    kind, n = _tokens(tokens, device)
+    if n != count:
+        raise ValueError(f"dy has {count} rows, tokens {n} elements")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return embedding_backward(dy, tokens, vocab, scale, out, dtype, accumulate, workspace)
+    out, ldo = _mx_result(out, vocab, width, dtype, device, "out")
+    if workspace is None:
+        workspace = torch.empty(max(embedding_workspace_bytes(count, vocab, width), 16), dtype=torch.uint8, device=device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device}")
+    _check(lib().bitopt_embedding_backward(dy.data_ptr(), dt, count, width, lddy, tokens.data_ptr(), kind, vocab, scale,
+                                           out.data_ptr(), _dt(out), ldo, 1 if accumulate else 0, workspace.data_ptr(),
+                                           workspace.numel(), _current(device)))
     return out

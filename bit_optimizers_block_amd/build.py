@@ -33,7 +33,8 @@ FLAGS = [
 SOURCES = ["bitopt_api.cpp", "codec.hip", "step_adam.hip", "step_ademamix.hip",
            "step_momentum.hip", "step_lion.hip", "step_rmsprop.hip", "step_adagrad.hip", "tensorwise.hip",
            "mx_api.cpp", "mx_codec.hip", "mx_linear.hip", "mx_grad.hip", "mx_skinny.hip",
-           "f8_api.cpp", "f8_codec.hip", "f8_fast.hip", "f8_exact.hip", "f8_few.hip"]
+           "f8_api.cpp", "f8_codec.hip", "f8_fast.hip", "f8_exact.hip", "f8_few.hip",
+           "layer_api.cpp", "layer_dropout.hip", "layer_embedding.hip"]
 
 
 def _compile(src: str, extra=()) -> str:

@@ -662,6 +662,67 @@ BITOPT_API int bitopt_f8_matmul(const uint8_t* a_codes, const float* a_scales, i
                                 int64_t m, int64_t n, int64_t k, void* out, int32_t out_dtype, int64_t ldo,
                                 int32_t accumulate, void* stream);
 
+/* ---------------------------------------------------------------- between the products
+ *
+ * Dropout, the embedding lookup and its gradient, with the conventions of the MX calls on
+ * sizes, distances of rows, graphs and equal bits on every run.
+ *
+ * Dropout whose mask is never stored.  T = round(65536 p) (ties to even); an element is kept
+ * when its 16 random bits are not below T, and multiplied by 65536 / (65536 - T); a dropped
+ * one is zero, whatever it holds.  The bits of row r, column c are half c % 2 (low half
+ * first) of word c % 8 / 2 of Philox4x32 with ten rounds (Salmon, Moraes, Dror, Shaw 2011),
+ * key (seed, seed >> 32), counter (c / 8, r, call, call >> 32), each word 32 bits.
+ *   forward    y = residual + dropout(x); residual NULL: y = dropout(x)
+ *   backward   dx = dropout(dy) with the forward's p, seed, call and counter (the
+ *              residual's gradient is dy itself)
+ *   call       tells apart the calls that share a seed: layers and steps
+ *   counter    device, 8-byte aligned, or NULL: its value is added to call when the kernel
+ *              runs, so a captured graph draws other bits at each replay once the caller
+ *              has advanced it
+ * y may be written over x or the residual, and dx over dy.  Arithmetic in fp32, rounded once
+ * (the product, then the sum, in fp32).  p outside [0, 1] gives INVALID_ARG.
+ */
+BITOPT_API int bitopt_dropout_forward(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                      const void* residual, int64_t ldr, double p, uint64_t seed, uint64_t call,
+                                      const uint64_t* counter, void* y, int64_t ldy, void* stream);
+BITOPT_API int bitopt_dropout_backward(const void* dy, int32_t dtype, int64_t rows, int64_t cols, int64_t lddy,
+                                       double p, uint64_t seed, uint64_t call, const uint64_t* counter, void* dx,
+                                       int64_t lddx, void* stream);
+
+/*
+ * Embedding lookup: out[t] = scale * table[tokens[t]], in fp32, rounded once into out_dtype.
+ * A token below 0 or not below vocab is padding: a row of zeros.  The table is vocab x width
+ * elements of dtype, or an MX matrix (the one that a tied vocabulary head's product reads).
+ *   tokens   device, `count` whole numbers of token_type
+ * scale has to be finite.
+ */
+#define BITOPT_TOKENS_I32 0
+#define BITOPT_TOKENS_I64 1
+BITOPT_API int bitopt_embedding_forward(const void* tokens, int32_t token_type, int64_t count, const void* table,
+                                        int32_t dtype, int64_t vocab, int64_t width, int64_t ldt, float scale,
+                                        void* out, int32_t out_dtype, int64_t ldo, void* stream);
+BITOPT_API int bitopt_mx_embedding_forward(const void* tokens, int32_t token_type, int64_t count,
+                                           const uint8_t* codes, const uint8_t* scales, int32_t format,
+                                           int64_t vocab, int64_t width, float scale, void* out, int32_t out_dtype,
+                                           int64_t ldo, void* stream);
+
+/*
+ * Its gradient: dtable[v] = scale * the sum of dy[t] over the tokens t with number v; rows
+ * without a token are zero.  accumulate != 0 adds the sums to dtable (a tied head's gradient,
+ * earlier micro-batches) and touches only rows that have a token.  Padding takes no
+ * part.  Tokens are sorted by number, each sum is taken in fp32 in the order of the batch (a
+ * frequent token's in parts, whose length follows from count), rounded once.
+ *   workspace   device, 16-byte aligned, at least bitopt_embedding_workspace_bytes(count,
+ *               vocab, width) bytes (-1: a size < 0 or above 2^30; no fewer for a larger
+ *               count), not needed between calls; calls that may run at the same time need
+ *               one each
+ */
+BITOPT_API int64_t bitopt_embedding_workspace_bytes(int64_t count, int64_t vocab, int64_t width);
+BITOPT_API int bitopt_embedding_backward(const void* dy, int32_t dtype, int64_t count, int64_t width, int64_t lddy,
+                                         const void* tokens, int32_t token_type, int64_t vocab, float scale,
+                                         void* dtable, int32_t out_dtype, int64_t ldd, int32_t accumulate,
+                                         void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
