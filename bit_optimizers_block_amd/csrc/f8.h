@@ -54,17 +54,18 @@ hipError_t launch_f8_few(const F8GemmArgs& g, int a_fmt, int b_fmt, int b_blocks
 
 template <int FMT> constexpr float kF8Top = FMT == kF8E4M3 ? 448.0f : 57344.0f;
 
-// Factor r = top / amax of a block from the bits of its largest |x|, with its significand cut
-// to 13 bits, and the scale 1 / r.  r <= top / amax (1 + 2^-24), so no element is above half a
-// step over the largest one and none saturates.  amax counts as top 2^-126 at least: r and 1 / r
-// stay normal numbers, and a block of zeros needs no case of its own.
+// Factor r = top (1 / amax) of a block from the bits of its largest |x|, both operations rounded,
+// with its significand then cut to 13 bits, and the scale 1 / r.  r <= top / amax (1 + 2^-21), also
+// where 1 / amax is subnormal, so no element is half a step above the largest one and none
+// saturates.  amax counts as top 2^-126 at least: r and 1 / r stay normal numbers, and a block of
+// zeros needs no case of its own.
 // An infinity or NaN in the block: the scale is NaN and r is zero.
 struct F8Scale {
     float r, s;
 };
 template <int FMT> __device__ __forceinline__ F8Scale f8_scale(uint32_t amax_bits) {
     const float amax = fmaxf(__uint_as_float(amax_bits), kF8Top<FMT> * 0x1p-126f);
-    const float r = __uint_as_float(__float_as_uint(kF8Top<FMT> / amax) & ~0x7ffu);
+    const float r = __uint_as_float(__float_as_uint(1.0f / amax * kF8Top<FMT>) & ~0x7ffu);
     const bool bad = amax_bits >= 0x7f800000u;
     return {bad ? 0.0f : r, bad ? __uint_as_float(0x7fc00000u) : 1.0f / r};
 }

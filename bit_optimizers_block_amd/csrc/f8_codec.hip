@@ -30,14 +30,17 @@ template <int DT, int FMT, bool TILES, bool T> __global__ __launch_bounds__(kThr
     for (int64_t block = blockIdx.y; block < rb; block += gridDim.y) {
         const int64_t r0 = block * B, r = r0 + 8 * rg;
         float v[8][8];
+        if (a.cols >= 8) {
+            Eight<DT> in[8];
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            if (r + p < a.rows) {
-                ld_eight<DT, false>(a.x, (r + p) * a.ldx + c, n, c, v[p]);
-            } else {
+            for (int p = 0; p < 8; ++p) in[p].template load<false>(a.x, min(r + p, a.rows - 1) * a.ldx, c, a.cols);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[p][j] = 0.0f;
-            }
+            for (int p = 0; p < 8; ++p) in[p].values(r + p < a.rows ? c + 8 - a.cols : 8, v[p]);
+        } else {
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[p][j] = r + p < a.rows && j < n ? load1<DT>(a.x, (r + p) * a.ldx + c + j) : 0.0f;
         }
         F8Scale all{};
         if constexpr (TILES) {
@@ -126,18 +129,24 @@ template <int DT, int FMT, bool TILES, bool T> __global__ __launch_bounds__(kThr
 }
 
 template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_f8_dequantize(F8CodecArgs a, RowGrid g, bool tiles) {
+    constexpr int PER = kPer<DT>;
     const int64_t cb = f8_blocks(a.cols);
-    for_items(g, a.rows, (int32_t)((a.cols + 7) / 8), [&](int64_t row, int32_t item) {
-        const int64_t c = 8 * (int64_t)item;
-        const u32x2 w = *gbl(reinterpret_cast<const u32x2*>(a.codes + row * cb * kF8Block + c));
+    for_items(g, a.rows, (int32_t)((a.cols + PER - 1) / PER), [&](int64_t row, int32_t item) {
+        const int64_t c = PER * (int64_t)item;
         const int64_t block = c / kF8Block;
         const float s = gbl(a.scales)[tiles ? row / kF8Block * cb + block : block * a.rows + row];
-        float v[8];
-        f8_decode4<FMT>(w.x, v);
-        f8_decode4<FMT>(w.y, v + 4);
+        const uint8_t* p = a.codes + row * cb * kF8Block + c;
+        float v[PER];
+        if constexpr (PER == 8) {
+            const u32x2 w = *gbl(reinterpret_cast<const u32x2*>(p));
+            f8_decode4<FMT>(w.x, v);
+            f8_decode4<FMT>(w.y, v + 4);
+        } else {
+            f8_decode4<FMT>(*gbl(reinterpret_cast<const uint32_t*>(p)), v);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s;
-        st_eight<DT>(a.out, row * a.ldo + c, (int)min((int64_t)8, a.cols - c), v);
+        for (int j = 0; j < PER; ++j) v[j] *= s;
+        st_item<DT>(a.out, row * a.ldo + c, (int)min((int64_t)PER, a.cols - c), v);
     });
 }
 
@@ -154,7 +163,7 @@ template <int DT, int FMT> static hipError_t quantize(const F8CodecArgs& a, bool
 
 template <int DT, int FMT> static hipError_t dequantize(const F8CodecArgs& a, bool tiles, hipStream_t s) {
     dim3 grid;
-    const RowGrid g = row_grid(a.rows, (a.cols + 7) / 8, grid);
+    const RowGrid g = row_grid(a.rows, (a.cols + kPer<DT> - 1) / kPer<DT>, grid);
     hipLaunchKernelGGL((k_f8_dequantize<DT, FMT>), grid, dim3(kThreads), 0, s, a, g, tiles);
     return hipGetLastError();
 }

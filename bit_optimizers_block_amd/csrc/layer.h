@@ -31,7 +31,7 @@ struct EmbeddingArgs {
 // Places in the workspace of an embedding's gradient, in bytes; every part is aligned to 16.
 struct EmbeddingSpace {
     int64_t keys[2], order[2], digits, partial, bytes;
-    int64_t span;                        // rows of one token that one workgroup adds up
+    int64_t span;                        // places of the sorted order in a window
 };
 
 struct EmbeddingGradArgs {

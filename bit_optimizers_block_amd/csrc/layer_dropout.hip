@@ -23,32 +23,34 @@ __device__ __forceinline__ u32x4 philox(u32x4 c, uint32_t k0, uint32_t k1) {
     return c;
 }
 
-// y may lie over x or the residual: a lane reads its eight elements before it writes them, and
-// what the last item's load takes from the item before is shifted out.  A dropped element is zero
-// whatever x holds there.
+// y may lie over x or the residual: a lane reads its elements before it writes them, and what the
+// last item's load takes from the item before is shifted out.  A dropped element is zero whatever x
+// holds there.  In fp32 a lane takes four elements, and two lanes draw the same eight.
 template <int DT, bool RESIDUAL> __global__ __launch_bounds__(kThreads) void k_dropout(DropoutArgs a, RowGrid g) {
+    constexpr int PER = kPer<DT>;
     const uint64_t call = a.call + (a.counter ? *a.counter : 0);
-    for_items(g, a.rows, (int32_t)((a.cols + 7) / 8), [&](int64_t row, int32_t item) {
-        const int64_t e = 8 * (int64_t)item;
-        const int n = (int)min((int64_t)8, a.cols - e);
-        float x[8], r[8];
-        ld_eight<DT, true>(a.x, row * a.ldx + e, n, e, x);
-        if constexpr (RESIDUAL) ld_eight<DT, true>(a.residual, row * a.ldr + e, n, e, r);
-        const u32x4 bits = philox(u32x4{(uint32_t)item, (uint32_t)row, (uint32_t)call, (uint32_t)(call >> 32)},
+    for_items(g, a.rows, (int32_t)((a.cols + PER - 1) / PER), [&](int64_t row, int32_t item) {
+        const int64_t e = PER * (int64_t)item;
+        const int n = (int)min((int64_t)PER, a.cols - e);
+        float x[PER], r[PER];
+        ld_item<DT, true>(a.x, row * a.ldx + e, n, e, x);
+        if constexpr (RESIDUAL) ld_item<DT, true>(a.residual, row * a.ldr + e, n, e, r);
+        const u32x4 bits = philox(u32x4{(uint32_t)(e / 8), (uint32_t)row, (uint32_t)call, (uint32_t)(call >> 32)},
                                   (uint32_t)a.seed, (uint32_t)(a.seed >> 32));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t u = j & 1 ? bits[j / 2] >> 16 : bits[j / 2] & 0xffffu;
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t w = PER == 8 ? bits[j / 2] : item & 1 ? bits[2 + j / 2] : bits[j / 2];
+            const uint32_t u = j & 1 ? w >> 16 : w & 0xffffu;
             x[j] = u >= a.threshold ? x[j] * a.grow : 0.0f;
             if constexpr (RESIDUAL) x[j] += r[j];
         }
-        st_eight<DT>(a.y, row * a.ldy + e, n, x);
+        st_item<DT>(a.y, row * a.ldy + e, n, x);
     });
 }
 
 template <int DT> static hipError_t dropout(const DropoutArgs& a, hipStream_t s) {
     dim3 grid;
-    const RowGrid g = row_grid(a.rows, (a.cols + 7) / 8, grid);
+    const RowGrid g = row_grid(a.rows, (a.cols + kPer<DT> - 1) / kPer<DT>, grid);
     if (a.residual) hipLaunchKernelGGL((k_dropout<DT, true>), grid, dim3(kThreads), 0, s, a, g);
     else hipLaunchKernelGGL((k_dropout<DT, false>), grid, dim3(kThreads), 0, s, a, g);
     return hipGetLastError();

@@ -2,9 +2,10 @@
 //
 // Gradient: out[v] (+)= scale * the sum of dy[t] over the tokens t with number v.  Tokens are
 // sorted by number with a stable radix sort, so the rows of one number are a run of the sorted
-// order, in their order in the batch: no atomics, and the same bits on every run.  A workgroup
-// adds up to `span` rows of a run in registers; longer runs (a frequent token) leave their parts
-// in the workspace, and a second kernel adds those.
+// order, in their order in the batch: no atomics, and the same bits on every run.  The order is
+// cut into windows of `span` places, each added up by one group of lanes with eight rows in
+// flight, whatever the runs' lengths; a run that lies in several windows (a frequent token)
+// leaves its parts in the workspace, and a second kernel adds those in their order.
 #include "launch.h"
 #include "layer.h"
 #include "mx_rows.h"
@@ -17,41 +18,43 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, bool wide, int64
     return wide ? gbl(reinterpret_cast<const int64_t*>(tokens))[t] : (int64_t)gbl(reinterpret_cast<const int32_t*>(tokens))[t];
 }
 
+// Elements of a lane: four where fp32 is written.
+template <int OUT> constexpr int kEach = OUT == kF32 ? 4 : 8;
+
 // A token outside the table gets zeros.
 template <int DT, int OUT> __global__ __launch_bounds__(kThreads) void k_embedding(EmbeddingArgs a, RowGrid g) {
-    for_items(g, a.count, (int32_t)((a.width + 7) / 8), [&](int64_t row, int32_t item) {
-        const int64_t e = 8 * (int64_t)item;
-        const int n = (int)min((int64_t)8, a.width - e);
+    constexpr int PER = kEach<OUT>;
+    for_items(g, a.count, (int32_t)((a.width + PER - 1) / PER), [&](int64_t row, int32_t item) {
+        const int64_t e = PER * (int64_t)item;
+        const int n = (int)min((int64_t)PER, a.width - e);
         const int64_t id = token_at(a.tokens, a.wide, row);
-        float v[8] = {};
-        if ((uint64_t)id < (uint64_t)a.vocab) ld_eight<DT, false>(a.table, id * a.ldt + e, n, e, v);
+        float v[PER] = {};
+        if ((uint64_t)id < (uint64_t)a.vocab) ld_row<DT, PER, false>(a.table, id * a.ldt + e, n, e, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= a.scale;
-        st_eight<OUT>(a.out, row * a.ldo + e, n, v);
+        for (int j = 0; j < PER; ++j) v[j] *= a.scale;
+        st_row<OUT, PER>(a.out, row * a.ldo + e, n, v);
     });
 }
 
 template <int FMT, int OUT> __global__ __launch_bounds__(kThreads) void k_mx_embedding(EmbeddingArgs a, RowGrid g) {
+    constexpr int PER = kEach<OUT>;
     const int64_t bytes = mx_code_bytes(a.width, FMT), blocks = mx_scale_bytes(a.width);
-    for_items(g, a.count, (int32_t)((a.width + 7) / 8), [&](int64_t row, int32_t item) {
+    for_items(g, a.count, (int32_t)((a.width + PER - 1) / PER), [&](int64_t row, int32_t item) {
         const int64_t id = token_at(a.tokens, a.wide, row);
-        float v[8] = {};
+        float v[PER] = {};
         if ((uint64_t)id < (uint64_t)a.vocab) {
-            const float s = mx_scale_f32(gbl(a.scales)[id * blocks + item / 4]);
-            const uint8_t* p = a.codes + id * bytes;
-            if constexpr (FMT == kMxE2M1) {
-                const uint32_t c = gbl(reinterpret_cast<const uint32_t*>(p))[item];
-                mx_decode4_e2m1(c, s, v);
-                mx_decode4_e2m1(c >> 16, s, v + 4);
-            } else {
-                const u32x2 c = gbl(reinterpret_cast<const u32x2*>(p))[item];
-                mx_decode4_e4m3(c.x, s, v);
-                mx_decode4_e4m3(c.y, s, v + 4);
+            const float s = mx_scale_f32(gbl(a.scales)[id * blocks + item / (kMxBlock / PER)]);
+            const uint8_t* p = a.codes + id * bytes + (int64_t)item * (FMT == kMxE2M1 ? PER / 2 : PER);
+#pragma unroll
+            for (int h = 0; h < PER / 4; ++h) {
+                if constexpr (FMT == kMxE2M1) mx_decode4_e2m1(gbl(reinterpret_cast<const uint16_t*>(p))[h], s, v + 4 * h);
+                else mx_decode4_e4m3(gbl(reinterpret_cast<const uint32_t*>(p))[h], s, v + 4 * h);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= a.scale;
-        st_eight<OUT>(a.out, row * a.ldo + 8 * (int64_t)item, (int)min((int64_t)8, a.width - 8 * (int64_t)item), v);
+        for (int j = 0; j < PER; ++j) v[j] *= a.scale;
+        const int64_t e = PER * (int64_t)item;
+        st_row<OUT, PER>(a.out, row * a.ldo + e, (int)min((int64_t)PER, a.width - e), v);
     });
 }
 
@@ -113,16 +116,23 @@ template <int WAVES> __device__ __forceinline__ void scan_counts(uint32_t* count
     }
 }
 
-// Zeros in every row of the gradient: `part` of `parts` workgroups.
+// Zeros in every row of the gradient: `part` of `parts` workgroups.  Rows without gaps are one.
 template <int OUT> __device__ __forceinline__ void clear_rows(const EmbeddingGradArgs& a, int64_t part, int64_t parts) {
-    const int32_t items = (int32_t)((a.width + 7) / 8);
+    constexpr int PER = kPer<OUT>;
+    const bool gaps = a.ldo != a.width;
+    const int64_t rows = gaps ? a.vocab : 1, width = gaps ? a.width : a.vocab * a.width, items = (width + PER - 1) / PER;
+    const float zero[PER] = {};
+    if (!gaps) {
+        for (int64_t i = part * blockDim.x + threadIdx.x; i < items; i += parts * blockDim.x)
+            st_item<OUT, false>(a.out, PER * i, (int)min((int64_t)PER, width - PER * i), zero);
+        return;
+    }
     int lanes = 64;
     while (lanes < (int)blockDim.x && lanes < items) lanes *= 2;
     const int per = (int)blockDim.x / lanes;
-    const float zero[8] = {};
-    for (int64_t row = part * per + threadIdx.x / lanes; row < a.vocab; row += parts * per)
-        for (int32_t item = threadIdx.x % lanes; item < items; item += lanes)
-            st_eight<OUT>(a.out, row * a.ldo + 8 * (int64_t)item, (int)min((int64_t)8, a.width - 8 * (int64_t)item), zero);
+    for (int64_t row = part * per + threadIdx.x / lanes; row < rows; row += parts * per)
+        for (int64_t i = threadIdx.x % lanes; i < items; i += lanes)
+            st_item<OUT, false>(a.out, row * a.ldo + PER * i, (int)min((int64_t)PER, width - PER * i), zero);
 }
 
 __device__ __forceinline__ uint32_t* in_work(const EmbeddingGradArgs& a, int64_t at) { return reinterpret_cast<uint32_t*>(a.work + at); }
@@ -263,115 +273,153 @@ __global__ __launch_bounds__(kThreads) void k_embedding_move(EmbeddingGradArgs a
 
 // -------------------------------------------------------------------------- the sums
 
-// First place in [lo, hi) whose key is not below `key`; keys are sorted.
-__device__ __forceinline__ int64_t first_not_below(const uint32_t* keys, int64_t lo, int64_t hi, uint32_t key) {
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (gbl(keys)[mid] < key) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
 template <int OUT>
 __device__ __forceinline__ void put_row(const EmbeddingGradArgs& a, uint32_t key, int32_t item, const float sum[8]) {
     const int64_t e = (int64_t)key * a.ldo + 8 * (int64_t)item;
     const int n = (int)min((int64_t)8, a.width - 8 * (int64_t)item);
     float v[8];
     if (a.accumulate) {
-        ld_eight<OUT, false>(a.out, e, n, 8 * (int64_t)item, v);
+        ld_row<OUT, 8, false>(a.out, e, n, 8 * (int64_t)item, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += sum[j] * a.scale;
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.scale;
     }
-    st_eight<OUT>(a.out, e, n, v);
+    st_row<OUT, 8, false>(a.out, e, n, v);
 }
 
-// Parts of long runs: a whole part that begins at place i lies in row 2 (i / span) of the partial
-// sums, a run's last one, if shorter, in the row behind it.  Two whole parts begin at least `span`
-// places apart, and so do two short ones of long runs.
-__device__ __forceinline__ float* part_row(const EmbeddingGradArgs& a, int64_t i, bool whole) {
-    return reinterpret_cast<float*>(a.work + a.at.partial) + (2 * (i / a.at.span) + !whole) * ((a.width + 7) / 8 * 8);
+// Window w's rows of partial sums: of the run that comes from the window before, and of one that
+// begins in it and goes on in the next.
+__device__ __forceinline__ float* part_row(const EmbeddingGradArgs& a, int64_t w, bool begins) {
+    return reinterpret_cast<float*>(a.work + a.at.partial) + (2 * w + begins) * ((a.width + 7) / 8 * 8);
 }
 
-// A place of the sorted order for each group of lanes: those where a part begins add up its rows.
-template <int DT, int OUT> __global__ __launch_bounds__(kThreads) void k_embedding_sums(EmbeddingGradArgs a, RowGrid g, int buffer) {
+// Up to eight rows at a time, all of them and, where sums are added to it, the gradient's rows
+// under way together.
+template <int DT, int OUT, bool ADD>
+__global__ __launch_bounds__(kThreads) void k_embedding_sums(EmbeddingGradArgs a, int lanes_log2, int buffer) {
+    constexpr int U = 8;
     const uint32_t *keys = in_work(a, a.at.keys[buffer]), *order = in_work(a, a.at.order[buffer]);
-    const int64_t span = a.at.span;
-    for_items(g, a.count, (int32_t)((a.width + 7) / 8), [&](int64_t i, int32_t item) {
-        const uint32_t key = gbl(keys)[i];
-        if (key >= (uint32_t)a.vocab) return;
-        bool whole_run = false;                         // the run is one part
-        if (i == 0 || gbl(keys)[i - 1] != key) {
-            whole_run = i + span >= a.count || gbl(keys)[i + span] != key;
-        } else {
-            if (i < span || gbl(keys)[i - span] != key) return;
-            if ((i - first_not_below(keys, 0, i - span, key)) % span != 0) return;
-        }
-        const int64_t last = min(i + span, a.count);
-        const int64_t end = gbl(keys)[last - 1] == key ? last : first_not_below(keys, i, last, key + 1);
-        const int64_t e = 8 * (int64_t)item;
-        const int n = (int)min((int64_t)8, a.width - e);
+    const int64_t span = a.at.span, windows = (a.count + span - 1) / span, per = kThreads >> lanes_log2;
+    const int32_t item = (int32_t)(blockIdx.x << lanes_log2) + (threadIdx.x & ((1 << lanes_log2) - 1));
+    const int64_t e = 8 * (int64_t)item, over = e + 8 - a.width;
+    if (over >= 8) return;
+    const uint32_t none = (uint32_t)a.vocab;
+    for (int64_t w = per * blockIdx.y + (threadIdx.x >> lanes_log2); w < windows; w += per * gridDim.y) {
+        const int64_t first = w * span, end = min(first + span, a.count);
+        uint32_t run = gbl(keys)[first];
+        // whether the run at hand began in this window
+        bool begins = first == 0 || gbl(keys)[first - 1] != run;
         float sum[8] = {};
-        int64_t r = i;
-        for (; r + 4 <= end; r += 4) {
-            float v[4][8];
+        for (int64_t i = first; i < end && run < none; i += U) {
+            uint32_t key[U + 1];
+            float v[U][8], old[ADD ? U : 1][8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ld_eight<DT, true>(a.dy, (int64_t)gbl(order)[r + k] * a.lddy + e, n, e, v[k]);
+            for (int k = 0; k <= U; ++k) {
+                const uint32_t at = gbl(keys)[min(i + k, a.count - 1)];
+                key[k] = i + k < a.count ? at : none;
+            }
+            if (a.width >= 8) {
+                Eight<DT> in[U];
+                Eight<OUT> was[ADD ? U : 1];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < U; ++k) {
+                    in[k].template load<false>(a.dy, (int64_t)gbl(order)[min(i + k, end - 1)] * a.lddy, e, a.width);
+                    if constexpr (ADD) was[k].template load<false>(a.out, (key[k] < none ? key[k] : 0) * a.ldo, e, a.width);
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    in[k].values(over, v[k]);
+                    if constexpr (ADD) was[k].values(over, old[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = j < a.width;
+                        v[k][j] = in ? load1<DT>(a.dy, (int64_t)gbl(order)[min(i + k, end - 1)] * a.lddy + j) : 0.0f;
+                        if constexpr (ADD) old[k][j] = in ? load1<OUT>(a.out, (key[k] < none ? key[k] : 0) * a.ldo + j) : 0.0f;
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (i + k >= end || key[k] >= none) break;
+                run = key[k];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] += v[k][j];
-        }
-        for (; r < end; ++r) {
-            float v[8];
-            ld_eight<DT, true>(a.dy, (int64_t)gbl(order)[r] * a.lddy + e, n, e, v);
+                if (key[k + 1] == run && i + k + 1 < end) continue;
+                // the run's last row here
+                if (begins && key[k + 1] != run) {
+                    float y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += v[j];
+                    for (int j = 0; j < 8; ++j) {
+                        y[j] = sum[j] * a.scale;
+                        if constexpr (ADD) y[j] = old[k][j] + y[j];
+                    }
+                    st_row<OUT, 8, false>(a.out, run * a.ldo + e, (int)min((int64_t)8, a.width - e), y);
+                } else {
+                    float* p = part_row(a, w, begins) + e;
+                    *gbl(reinterpret_cast<f32x4*>(p)) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+                    *gbl(reinterpret_cast<f32x4*>(p + 4)) = f32x4{sum[4], sum[5], sum[6], sum[7]};
+                }
+                begins = true;
+                run = key[k + 1];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+            }
         }
-        if (whole_run) {
-            put_row<OUT>(a, key, item, sum);
-        } else {
-            float* p = part_row(a, i, end - i == span) + e;
-            *gbl(reinterpret_cast<f32x4*>(p)) = f32x4{sum[0], sum[1], sum[2], sum[3]};
-            *gbl(reinterpret_cast<f32x4*>(p + 4)) = f32x4{sum[4], sum[5], sum[6], sum[7]};
-        }
-    });
+    }
 }
 
-// `span` places of the sorted order for each workgroup: at most one run of more than a part begins
-// there, and its parts are added up.
-template <int OUT> __global__ __launch_bounds__(kThreads) void k_embedding_join(EmbeddingGradArgs a, int buffer) {
-    __shared__ int64_t begins;
+constexpr int kJoinThreads = 512;
+
+// Adds up the parts of the run that begins in a window and goes on in the next, if there is one:
+// each group of lanes a stretch of them, the groups' sums in LDS in their order.
+template <int OUT> __global__ __launch_bounds__(kJoinThreads) void k_embedding_join(EmbeddingGradArgs a, int lanes_log2, int buffer) {
+    __shared__ f32x4 sums[2][kJoinThreads];
     const uint32_t* keys = in_work(a, a.at.keys[buffer]);
     const int64_t span = a.at.span, windows = (a.count + span - 1) / span;
-    for (int64_t w = blockIdx.x; w < windows; w += gridDim.x) {
-        __syncthreads();
-        if (threadIdx.x == 0) begins = -1;
-        __syncthreads();
-        for (int64_t i = w * span + threadIdx.x; i < min((w + 1) * span, a.count - span); i += kThreads) {
-            const uint32_t key = gbl(keys)[i];
-            if (key < (uint32_t)a.vocab && (i == 0 || gbl(keys)[i - 1] != key) && gbl(keys)[i + span] == key) begins = i;
+    const int lanes = 1 << lanes_log2, groups = kJoinThreads >> lanes_log2;
+    const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x >> lanes_log2;
+    for (int64_t w = blockIdx.x; w + 1 < windows; w += gridDim.x) {
+        const int64_t first = w * span;
+        const uint32_t run = gbl(keys)[first + span];
+        if (run >= (uint32_t)a.vocab || gbl(keys)[first + span - 1] != run) continue;
+        if (first > 0 && gbl(keys)[first - 1] == run) continue;
+        // windows that begin with the run: w + 1 and those behind it without a gap
+        int64_t parts = 1;
+        for (int64_t v = w + 1; v < windows; v += 64) {
+            const int64_t at = (v + (threadIdx.x & 63)) * span;
+            const uint64_t other = __ballot(at >= a.count || gbl(keys)[min(at, a.count - 1)] != run);
+            parts += other ? __builtin_ctzll(other) : 64;
+            if (other) break;
         }
-        __syncthreads();
-        if (begins < 0) continue;
-        const int64_t first = begins;
-        const uint32_t key = gbl(keys)[first];
-        const int64_t end = first_not_below(keys, first, a.count, key + 1);
-        for (int32_t item = threadIdx.x; item < (int32_t)((a.width + 7) / 8); item += kThreads) {
-            float sum[8] = {};
-            for (int64_t i = first; i < end; i += span) {
-                const float* p = part_row(a, i, end - i >= span) + 8 * (int64_t)item;
-                const f32x4 lo = *gbl(reinterpret_cast<const f32x4*>(p)), hi = *gbl(reinterpret_cast<const f32x4*>(p + 4));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum[j] += lo[j];
-                    sum[4 + j] += hi[j];
+        const int64_t stretch = (parts + groups - 1) / groups, lo = group * stretch, hi = min(lo + stretch, parts);
+        for (int64_t c = lane; c < (int64_t)((a.width + 7) / 8 + lanes - 1) / lanes * lanes; c += lanes) {
+            const bool in = c < (a.width + 7) / 8;
+            f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+            if (in) {
+#pragma unroll 8
+                for (int64_t v = lo; v < hi; ++v) {
+                    const float* p = part_row(a, w + v, v == 0) + 8 * c;
+                    s0 += *gbl(reinterpret_cast<const f32x4*>(p));
+                    s1 += *gbl(reinterpret_cast<const f32x4*>(p + 4));
                 }
             }
-            put_row<OUT>(a, key, item, sum);
+            __syncthreads();                // the last columns' sums have been read
+            sums[0][threadIdx.x] = s0;
+            sums[1][threadIdx.x] = s1;
+            __syncthreads();
+            if (group == 0 && in) {
+                for (int k = 1; k < groups && k * stretch < parts; ++k) {
+                    s0 += sums[0][k * lanes + lane];
+                    s1 += sums[1][k * lanes + lane];
+                }
+                const float sum[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                put_row<OUT>(a, run, (int32_t)c, sum);
+            }
         }
     }
 }
@@ -390,11 +438,13 @@ static bool small_sort(int64_t count, int64_t vocab) {
     return count <= 16 * kSmallThreads && place_bits(count) + bits_of(vocab) <= 32;
 }
 
+constexpr int64_t kWindows = 2048;
+
 EmbeddingSpace embedding_space(int64_t count, int64_t vocab, int64_t width) {
     EmbeddingSpace s{};
-    // a run of all tokens is twice as many parts as a part has rows, at most
-    s.span = 32;
-    while (4 * s.span * s.span < count) s.span *= 2;
+    // eight rows are one round of loads; 2048 windows are enough for every CU, and few parts to join
+    s.span = 8;
+    while (kWindows * s.span < count) s.span *= 2;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t p = at;
@@ -407,8 +457,8 @@ EmbeddingSpace embedding_space(int64_t count, int64_t vocab, int64_t width) {
         s.order[b] = take(4 * count);
     }
     if (!small) s.digits = take(4 * kDigits * ((count + kTileItems - 1) / kTileItems));
-    // not less than fewer tokens take, whose parts are shorter: a workspace for a count serves all below
-    const int64_t parts = std::max<int64_t>(2 * ((count + s.span - 1) / s.span), s.span > 32 ? 4 * s.span : 0);
+    // not less than fewer tokens take, whose windows are shorter: a workspace for a count serves all below
+    const int64_t parts = std::max<int64_t>(2 * ((count + s.span - 1) / s.span), s.span > 8 ? 2 * kWindows : 0);
     if (count > s.span) s.partial = take(parts * ((width + 7) / 8 * 8) * 4);
     s.bytes = at;
     return s;
@@ -440,19 +490,26 @@ template <int OUT> static hipError_t sort_tokens(const EmbeddingGradArgs& a, int
     return hipSuccess;
 }
 
+template <int DT, int OUT> static void sums(const EmbeddingGradArgs& a, dim3 grid, int lanes_log2, int buffer, hipStream_t s) {
+    if (a.accumulate) hipLaunchKernelGGL((k_embedding_sums<DT, OUT, true>), grid, dim3(kThreads), 0, s, a, lanes_log2, buffer);
+    else hipLaunchKernelGGL((k_embedding_sums<DT, OUT, false>), grid, dim3(kThreads), 0, s, a, lanes_log2, buffer);
+}
+
 template <int OUT> static hipError_t embedding_grad(const EmbeddingGradArgs& a, int dtype, hipStream_t s) {
     int buffer;
     if (hipError_t e = sort_tokens<OUT>(a, buffer, s)) return e;
     if (a.count == 0) return hipSuccess;
-    dim3 grid;
-    const RowGrid g = row_grid(a.count, (a.width + 7) / 8, grid);
-    if (dtype == kF32) hipLaunchKernelGGL((k_embedding_sums<kF32, OUT>), grid, dim3(kThreads), 0, s, a, g, buffer);
-    else if (dtype == kF16) hipLaunchKernelGGL((k_embedding_sums<kF16, OUT>), grid, dim3(kThreads), 0, s, a, g, buffer);
-    else hipLaunchKernelGGL((k_embedding_sums<kBF16, OUT>), grid, dim3(kThreads), 0, s, a, g, buffer);
-    if (a.count > a.at.span) {
-        const int64_t windows = (a.count + a.at.span - 1) / a.at.span;
-        hipLaunchKernelGGL((k_embedding_join<OUT>), dim3((unsigned)std::min<int64_t>(windows, 65535)), dim3(kThreads), 0, s, a, buffer);
-    }
+    const int64_t windows = (a.count + a.at.span - 1) / a.at.span, items = (a.width + 7) / 8;
+    int lanes_log2 = 4;
+    while (lanes_log2 < 8 && (1 << lanes_log2) < items) ++lanes_log2;
+    const int64_t per = kThreads >> lanes_log2;
+    const dim3 grid((unsigned)((items + (1 << lanes_log2) - 1) >> lanes_log2), (unsigned)std::min<int64_t>((windows + per - 1) / per, 65535));
+    if (dtype == kF32) sums<kF32, OUT>(a, grid, lanes_log2, buffer, s);
+    else if (dtype == kF16) sums<kF16, OUT>(a, grid, lanes_log2, buffer, s);
+    else sums<kBF16, OUT>(a, grid, lanes_log2, buffer, s);
+    if (windows > 1)
+        hipLaunchKernelGGL((k_embedding_join<OUT>), dim3((unsigned)std::min<int64_t>(windows - 1, 65535)), dim3(kJoinThreads), 0, s, a,
+                           lanes_log2, buffer);
     return hipGetLastError();
 }
 
@@ -463,7 +520,8 @@ hipError_t launch_embedding_grad(const EmbeddingGradArgs& a, int dtype, int out_
 
 template <int DT> static hipError_t embedding(const EmbeddingArgs& a, int out_dtype, hipStream_t s) {
     dim3 grid;
-    const RowGrid g = row_grid(a.count, (a.width + 7) / 8, grid);
+    const int per = out_dtype == kF32 ? 4 : 8;
+    const RowGrid g = row_grid(a.count, (a.width + per - 1) / per, grid);
     if (out_dtype == kF32) hipLaunchKernelGGL((k_embedding<DT, kF32>), grid, dim3(kThreads), 0, s, a, g);
     else if (out_dtype == kF16) hipLaunchKernelGGL((k_embedding<DT, kF16>), grid, dim3(kThreads), 0, s, a, g);
     else hipLaunchKernelGGL((k_embedding<DT, kBF16>), grid, dim3(kThreads), 0, s, a, g);
@@ -476,7 +534,8 @@ hipError_t launch_embedding(const EmbeddingArgs& a, int dtype, int out_dtype, hi
 
 template <int FMT> static hipError_t mx_embedding(const EmbeddingArgs& a, int out_dtype, hipStream_t s) {
     dim3 grid;
-    const RowGrid g = row_grid(a.count, (a.width + 7) / 8, grid);
+    const int per = out_dtype == kF32 ? 4 : 8;
+    const RowGrid g = row_grid(a.count, (a.width + per - 1) / per, grid);
     if (out_dtype == kF32) hipLaunchKernelGGL((k_mx_embedding<FMT, kF32>), grid, dim3(kThreads), 0, s, a, g);
     else if (out_dtype == kF16) hipLaunchKernelGGL((k_mx_embedding<FMT, kF16>), grid, dim3(kThreads), 0, s, a, g);
     else hipLaunchKernelGGL((k_mx_embedding<FMT, kBF16>), grid, dim3(kThreads), 0, s, a, g);

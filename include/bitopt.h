@@ -625,9 +625,9 @@ BITOPT_API int64_t bitopt_f8_scale_count(int64_t rows, int64_t cols, int32_t blo
 
 /*
  * Quantization to F8.  With top the format's largest value and amax the block's largest |x|,
- * at least top 2^-126: r = top / amax in fp32, its significand cut to 13 bits; codes are x r
- * rounded to nearest, ties to the even code, signs kept (also of zero); the scale is 1 / r in
- * fp32.  No element saturates.  A block that holds an infinity or a NaN gets the scale NaN
+ * at least top 2^-126: r = top (1 / amax), both operations rounded to fp32, its significand
+ * then cut to 13 bits; codes are x r rounded to nearest, ties to the even code, signs kept (also
+ * of zero); the scale is 1 / r in fp32.  No element saturates.  A block that holds an infinity or a NaN gets the scale NaN
  * and zero codes: all of it decodes to NaN.
  *   codes, scales       the matrix, or both NULL
  *   codes_t, scales_t   its transpose (cols x rows, blocks along the columns of x), or both
@@ -710,8 +710,8 @@ BITOPT_API int bitopt_mx_embedding_forward(const void* tokens, int32_t token_typ
  * Its gradient: dtable[v] = scale * the sum of dy[t] over the tokens t with number v; rows
  * without a token are zero.  accumulate != 0 adds the sums to dtable (a tied head's gradient,
  * earlier micro-batches) and touches only rows that have a token.  Padding takes no
- * part.  Tokens are sorted by number, each sum is taken in fp32 in the order of the batch (a
- * frequent token's in parts, whose length follows from count), rounded once.
+ * part.  Tokens are sorted by number, each sum is taken in fp32 in the order of the batch (in
+ * parts where the sorted order is cut, at places that follow from count), rounded once.
  *   workspace   device, 16-byte aligned, at least bitopt_embedding_workspace_bytes(count,
  *               vocab, width) bytes (-1: a size < 0 or above 2^30; no fewer for a larger
  *               count), not needed between calls; calls that may run at the same time need

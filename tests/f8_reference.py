@@ -38,7 +38,7 @@ def factors(x, fmt, blocks):
     amax = full.reshape(full.shape[0] // high, high, -1, BLOCK).max((1, 3))
     top = TOP[fmt]
     with np.errstate(invalid="ignore"):
-        r = np.float32(top) / np.maximum(amax, top * 2.0**-126).astype(np.float32)      # fp32 division
+        r = np.float32(1) / np.maximum(amax, top * 2.0**-126).astype(np.float32) * np.float32(top)    # both in fp32
     r = (r.view(np.uint32) & np.uint32(~0x7ff & 0xffffffff)).view(np.float32).astype(float)
     r = np.where(np.isfinite(amax), r, np.nan)
     with np.errstate(invalid="ignore"):
