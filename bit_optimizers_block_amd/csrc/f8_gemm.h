@@ -10,6 +10,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "f8.h"
 
@@ -20,29 +21,48 @@ template <int AF, int BF> __device__ __forceinline__ f32x4 mfma_f8(i32x8 a, i32x
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, AF, BF, 0, 0, 0, 0);
 }
 
-// Waits for the wave's loads and LDS accesses, then for the workgroup.  The empty statements
-// keep memory accesses on their side.
-__device__ __forceinline__ void f8_barrier() {
+// Waits until at most N of the wave's global loads are outstanding and its LDS reads are done, then
+// for the workgroup.  The empty statements keep memory accesses on their side.
+template <int N> __device__ __forceinline__ void f8_barrier() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x70);
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// Workgroup tile BM x BN, wave tile WM x WN, two LDS buffers of one block of 128 contraction
-// elements: rows of 128 bytes, filled by direct loads while the other buffer is multiplied, one
-// barrier a block.  A wave's load fills 1024 consecutive bytes of LDS, so the swizzle that spreads
-// a fragment's rows over the banks -- 16-byte chunk c of row r lies at chunk c ^ (r % 8) -- is
-// applied to the source address.  A lane holds row l % 16 and chunks q and q + 4, q = l / 16, of
-// either operand: which elements those are does not matter to the sum, as long as both agree.
-template <int AF, int BF, bool BTILES, bool EXACT, int BM, int BN, int WM, int WN>
+// SIZE bytes for each lane from a uniform base and the lane's offset to LDS, the wave's one behind the
+// other.  A buffer load: its address takes one register, and the compiler counts it apart from the
+// LDS reads, where after a global load to LDS it waits for all of them at each.
+template <int SIZE> __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, char* to) {
+#ifdef __HIP_DEVICE_COMPILE__
+    const auto from = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, -1, 0x00027000);
+    const auto at = (__attribute__((address_space(3))) void*)to;
+    if constexpr (SIZE == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(from, at, 16, offset, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(from, at, 4, offset, 0, 0, 0);
+#endif
+}
+
+// Workgroup tile BM x BN, wave tile WM x WN, NS LDS buffers of one block of 128 contraction elements:
+// rows of 128 bytes, filled by direct loads NS - 1 blocks ahead.  A wave's load fills 1024
+// consecutive bytes of LDS, so the swizzle that spreads a fragment's rows over the banks -- 16-byte
+// chunk c of row r lies at chunk c ^ (r % 8) -- is applied to the source address.  A lane holds row
+// l % 16 and chunks q and q + 4, q = l / 16, of either operand: which elements those are does not
+// matter to the sum, as long as both agree.
+//
+// A block goes in groups of one A fragment by all of B's; under a group's products run the reads of
+// a later A fragment and the additions of the group before.  Where every fragment left is in
+// registers the barrier that ends the block stands, and its buffer is filled anew.  Fast: that is
+// ahead of the last two groups, which go column by column, so that B's fragments are free one after
+// the other for the reads of the next block.  Exact: ahead of the last group; B's decoded fragments
+// leave no registers for the next ones.
+template <int AF, int BF, bool BTILES, bool EXACT, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;
-    constexpr int STAGE = (BM + BN) * 128, PASS_ROWS = NT / 8, LOADS = (BM + BN) / PASS_ROWS;
-    constexpr int SCALES = (BM + (BTILES ? 0 : BN)) * 4;
+    constexpr int ROWS = (BM + BN) * 128, PASS_ROWS = NT / 8, LOADS = (BM + BN) / PASS_ROWS;
+    constexpr int STAGE = ROWS + NT * 4;                // a scale for each thread: A's rows, then B's rows or tiles
     static_assert(BM % PASS_ROWS == 0 && BN % PASS_ROWS == 0 && PASS_ROWS % 8 == 0, "whole passes per operand");
-    static_assert(BM + BN <= NT && kF8Block % WN == 0, "a scale for each thread at most; a wave's columns in one tile");
-    __shared__ __attribute__((aligned(16))) char lds[2 * STAGE + 2 * SCALES];
+    static_assert((BTILES ? BM + 64 : BM + BN) <= NT && kF8Block % WN == 0, "a wave's columns lie in one tile");
+    __shared__ __attribute__((aligned(16))) char lds[NS * STAGE];
 
     int tm, tn;
     mx_tile((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn);
@@ -64,24 +84,26 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
         off[i] = (uint32_t)(i * PASS_ROWS < BM ? min(r, g.M - 1 - m0) : min(r - BM, g.N - 1 - n0)) * (uint32_t)g.row_bytes +
                  chunk * 16;
     }
-    const float* s_next = tid < BM ? g.a_scales + min(m0 + tid, g.M - 1) : g.b_scales + min(n0 + tid - BM, g.N - 1);
-    const int64_t s_step = tid < BM ? g.M : g.N;
-    auto issue = [&](int buffer) {
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds(
-                (const BITOPT_GLOBAL void*)((i * PASS_ROWS < BM ? a_next : b_next) + off[i]),
-                (__attribute__((address_space(3))) void*)(lds + buffer * STAGE + i * NT * 16 + wave * 1024), 16, 0, 0);
-        if (wave * 256 < SCALES)
-            __builtin_amdgcn_global_load_lds(
-                (const BITOPT_GLOBAL void*)s_next,
-                (__attribute__((address_space(3))) void*)(lds + 2 * STAGE + buffer * SCALES + wave * 256), 4, 0, 0);
-        a_next += kF8Block;
-        b_next += kF8Block;
-        s_next += s_step;
+    // this thread's scale of a block (a wave's are all A's or all B's), and how far the next block's is
+    const bool of_a = wave * 64 < BM;
+    const int sr = of_a ? tid : tid - BM;
+    const float* s_next = of_a ? g.a_scales + m0 : BTILES ? g.b_scales + (int64_t)(n0 / kF8Block) * steps : g.b_scales + n0;
+    const int64_t s_step = of_a ? g.M : BTILES ? 1 : g.N;
+    const uint32_t s_off = 4u * (of_a ? (uint32_t)min(sr, g.M - 1 - m0)
+                                      : BTILES ? (uint32_t)min(sr, (g.N - 1) / kF8Block - n0 / kF8Block) * (uint32_t)steps
+                                               : (uint32_t)min(sr, g.N - 1 - n0));
+    // LOADS + 1 loads of each wave; after the last block they repeat it, into buffers that are not read
+    auto load = [&](int buffer, int i) {
+        char* to = lds + buffer * STAGE;
+        if (i < LOADS) load_to_lds<16>(i * PASS_ROWS < BM ? a_next : b_next, off[i], to + i * NT * 16 + wave * 1024);
+        else load_to_lds<4>(s_next, s_off, to + ROWS + wave * 256);
     };
-    // the wave's columns lie in one tile of 128; beyond the last, one whose results are not stored
-    const float* b_tile = g.b_scales + (int64_t)min((n0 + wn) / kF8Block, (g.N - 1) / kF8Block) * steps;
+    auto advance = [&](int t) {
+        const bool more = t + 1 < steps;
+        a_next += more ? kF8Block : 0;
+        b_next += more ? kF8Block : 0;
+        s_next += more ? s_step : 0;
+    };
 
     f32x4 acc[FM][FN];
 #pragma unroll
@@ -89,73 +111,167 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (steps > 0) {
-        issue(0);
-        f8_barrier();
-    }
-    for (int t = 0; t < steps; ++t) {
-        const int buffer = t & 1;
-        if (t + 1 < steps) issue(buffer ^ 1);
-        const char* cur = lds + buffer * STAGE + li * 128;
-        const float* sc = reinterpret_cast<const float*>(lds + 2 * STAGE + buffer * SCALES);
-        const int lo = (q ^ (li & 7)) << 4, hi = ((q + 4) ^ (li & 7)) << 4;
-        auto read = [&](int row, u32x4& x, u32x4& y) {
-            x = *reinterpret_cast<const u32x4*>(cur + row * 128 + lo);
-            y = *reinterpret_cast<const u32x4*>(cur + row * 128 + hi);
-        };
-        float tile = 0.0f;
-        f32x4 sb[BTILES ? 1 : FN];
+    struct Codes {
+        u32x4 x, y;
+    };
+    const int lo = (q ^ (li & 7)) << 4, hi = ((q + 4) ^ (li & 7)) << 4;
+    const uint32_t a_at = (wm + li) * 128, b_at = (BM + wn + li) * 128, sa_at = ROWS + (wm + li) * 4;
+    const uint32_t sb_at = ROWS + (BM + (BTILES ? wn / kF8Block : wn + 4 * q)) * 4;
+    auto read_a = [&](const char* cur, int i) {
+        return Codes{*reinterpret_cast<const u32x4*>(cur + a_at + lo + i * 2048), *reinterpret_cast<const u32x4*>(cur + a_at + hi + i * 2048)};
+    };
+    auto read_b = [&](const char* cur, int j) {
+        return Codes{*reinterpret_cast<const u32x4*>(cur + b_at + lo + j * 2048), *reinterpret_cast<const u32x4*>(cur + b_at + hi + j * 2048)};
+    };
+    auto read_sa = [&](const char* cur, int i) { return *reinterpret_cast<const float*>(cur + sa_at + i * 64); };
+    f32x4 sb[BTILES ? 1 : FN];
+    auto read_sb = [&](const char* cur) {
         if constexpr (BTILES) {
-            tile = b_tile[t];
+            sb[0].x = *reinterpret_cast<const float*>(cur + sb_at);
         } else {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(sc + BM + wn + 16 * j + 4 * q);
+            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(cur + sb_at + j * 64);
         }
-        u32x4 bx[FN], by[FN];
+    };
+    // acc[i][j] += a product times its scales
+    auto add = [&](int i, int j, f32x4 p, float scale) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) read(BM + wn + 16 * j, bx[j], by[j]);
-        u32x4 bh[EXACT ? FN : 1][4];
-        if constexpr (EXACT) {
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], BTILES ? scale : scale * sb[j][r], acc[i][j][r]);
+    };
+    auto eight = [](const Codes& c) {
+        return i32x8{(int)c.x.x, (int)c.x.y, (int)c.x.z, (int)c.x.w, (int)c.y.x, (int)c.y.y, (int)c.y.z, (int)c.y.w};
+    };
+
+    static_assert(FM % 2 == 0, "fragments in pairs");
+    Codes a[2], b[FN];
+    float sa[2];
+    auto halves = [](const Codes& c, auto fmt, u32x4 h[4]) {
+        constexpr int F = decltype(fmt)::value;
+        h[0] = f8_half8<F>(c.x.x, c.x.y); h[1] = f8_half8<F>(c.x.z, c.x.w);
+        h[2] = f8_half8<F>(c.y.x, c.y.y); h[3] = f8_half8<F>(c.y.z, c.y.w);
+    };
+    constexpr std::integral_constant<int, AF> af;
+    constexpr std::integral_constant<int, BF> bf;
+    if (steps > 0) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                bh[j][0] = f8_half8<BF>(bx[j].x, bx[j].y); bh[j][1] = f8_half8<BF>(bx[j].z, bx[j].w);
-                bh[j][2] = f8_half8<BF>(by[j].x, by[j].y); bh[j][3] = f8_half8<BF>(by[j].z, by[j].w);
-            }
+        for (int s = 0; s < NS; ++s) {
+#pragma unroll
+            for (int i = 0; i <= LOADS; ++i) load(s, i);
+            advance(s);
+            asm volatile("" ::: "memory");              // in this order: the waits count on it
         }
+        f8_barrier<(NS - 1) * (LOADS + 1)>();
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            u32x4 ax, ay;
-            read(wm + 16 * i, ax, ay);
-            float sa = sc[wm + 16 * i + li];
-            if constexpr (BTILES) sa *= tile;
-            u32x4 ah[4];
-            if constexpr (EXACT) {
-                ah[0] = f8_half8<AF>(ax.x, ax.y); ah[1] = f8_half8<AF>(ax.z, ax.w);
-                ah[2] = f8_half8<AF>(ay.x, ay.y); ah[3] = f8_half8<AF>(ay.z, ay.w);
-            }
-            // B first: a lane then holds four consecutive columns of one output row
+        for (int j = 0; j < FN; ++j) b[j] = read_b(lds, j);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (EXACT) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) p = mfma16<kBF16>(bh[j][h], ah[h], p);
-                } else {
-                    const i32x8 x = {(int)bx[j].x, (int)bx[j].y, (int)bx[j].z, (int)bx[j].w,
-                                     (int)by[j].x, (int)by[j].y, (int)by[j].z, (int)by[j].w};
-                    const i32x8 y = {(int)ax.x, (int)ax.y, (int)ax.z, (int)ax.w, (int)ay.x, (int)ay.y, (int)ay.z, (int)ay.w};
-                    p = mfma_f8<BF, AF>(x, y, p);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (BTILES) acc[i][j][r] = __builtin_fmaf(p[r], sa, acc[i][j][r]);
-                    else acc[i][j][r] = __builtin_fmaf(p[r], sa * sb[j][r], acc[i][j][r]);
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+            a[i] = read_a(lds, i);
+            sa[i] = read_sa(lds, i);
         }
-        // the next block has to be there, and every wave to have read this one
-        f8_barrier();
+        read_sb(lds);
     }
+    int buffer = 0;
+    for (int t = 0; t < steps; ++t) {
+        const char* cur = lds + buffer * STAGE;
+        const int after = buffer + 1 == NS ? 0 : buffer + 1;
+        const char* next = lds + after * STAGE;
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 p[2][FN];
+        float scale[2];
+        // the next block has to be there, and every wave to have read this one
+        auto turn = [&] {
+            f8_barrier<(NS - 2) * (LOADS + 1)>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // B first: a lane then holds four consecutive columns of one output row
+        if constexpr (!EXACT) {
+#pragma unroll
+            for (int i = 0; i < FM - 2; ++i) {
+                scale[i & 1] = BTILES ? sa[i & 1] * sb[0].x : sa[i & 1];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    p[i & 1][j] = mfma_f8<BF, AF>(eight(b[j]), eight(a[i & 1]), zero);
+                    if (i > 0) add(i - 1, j, p[(i - 1) & 1][j], scale[(i - 1) & 1]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                a[i & 1] = read_a(cur, i + 2);
+                sa[i & 1] = read_sa(cur, i + 2);
+                asm volatile("" ::: "memory");          // the reads stay ahead of the next products
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            turn();
+            float left[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) left[k] = BTILES ? sa[k] * sb[0].x : sa[k];
+            f32x4 r[2][2];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    r[j & 1][k] = mfma_f8<BF, AF>(eight(b[j]), eight(a[k]), zero);
+                    if (j > 0) add(FM - 2 + k, j - 1, r[1 - (j & 1)][k], left[k]);
+                    else if constexpr (FM > 2)
+#pragma unroll
+                        for (int l = k * FN / 2; l < (k + 1) * FN / 2; ++l) add(FM - 3, l, p[(FM - 3) & 1][l], scale[(FM - 3) & 1]);
+                    if (k == 1) b[j] = read_b(next, j);
+                    if (j + 1 == FN) {
+                        a[k] = read_a(next, k);
+                        sa[k] = read_sa(next, k);
+                    }
+#pragma unroll
+                    for (int l = (2 * j + k) * (LOADS + 1) / (2 * FN); l < (2 * j + k + 1) * (LOADS + 1) / (2 * FN); ++l) load(buffer, l);
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) add(FM - 2 + k, FN - 1, r[(FN - 1) & 1][k], left[k]);
+        } else {
+            u32x4 bh[FN][4];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) halves(b[j], bf, bh[j]);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                scale[i & 1] = BTILES ? sa[i & 1] * sb[0].x : sa[i & 1];
+                u32x4 ah[4];
+                halves(a[i & 1], af, ah);
+                if (i + 2 < FM) {
+                    a[i & 1] = read_a(cur, i + 2);
+                    sa[i & 1] = read_sa(cur, i + 2);
+                }
+                if (i + 1 == FM) {
+                    turn();
+#pragma unroll
+                    for (int l = 0; l <= LOADS; ++l) load(buffer, l);
+                }
+                asm volatile("" ::: "memory");          // the reads stay ahead of the products
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) p[i & 1][j] = mfma16<kBF16>(bh[j][h], ah[h], h ? p[i & 1][j] : zero);
+#pragma unroll
+                    for (int j = h * FN / 4; j < (h + 1) * FN / 4; ++j)
+                        if (i > 0) add(i - 1, j, p[(i - 1) & 1][j], scale[(i - 1) & 1]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) b[j] = read_b(next, j);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                a[k] = read_a(next, k);
+                sa[k] = read_sa(next, k);
+            }
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < FN; ++j) add(FM - 1, j, p[(FM - 1) & 1][j], scale[(FM - 1) & 1]);
+        }
+        read_sb(next);
+        advance(t + NS);
+        buffer = after;
+    }
+    f8_barrier<0>();                    // no load to LDS outlives its workgroup
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + wm + 16 * i + li;
@@ -166,14 +282,64 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
 
 // ------------------------------------------------------------------------ tile choice
 
+// The form that is estimated to take the least time for a block of contraction: `one` us for up to 256
+// tiles (one a CU), else `two` for each 512; of the largest form one workgroup fills a CU.  Measured us of whole products with each form, 16-bit
+// results, B by tiles:
+//   M x N x K            256 x 256   128 x 128   128 x 64   64 x 64
+//   8192 x 8192 x 2048   152         185         257        282
+//   8192 x 2048 x 8192   117         145         194        225
+//   4096 x 4096 x 4096   60          76          103        122
+//   2048 x 2048 x 2048               13.9        16.7       20.0
+//   1024 x 4096 x 4096   47          26.8        25.8       31.9
+//   1024 x 2048 x 8192   86          43          28.5       32.6
+//   512 x 2048 x 2048    27          10.7        8.3        7.5
+//   128 x 2048 x 8192    83          32          21.5       20.5
+//   777 x 1001 x 513                 7.1         5.5        4.6
+// and with fp32 results, B by rows:
+//   M x N x K            256 x 128   128 x 64    64 x 64
+//   8192 x 2048 x 8192   249         303         380
+//   4096 x 4096 x 4096   130         161         202
+//   1024 x 4096 x 4096   64          42          53
+//   1024 x 2048 x 8192   117         44          52
+//   512 x 2048 x 2048    34          13.5        11.8
+//   128 x 2048 x 8192    112         42          37
+struct F8Form {
+    int bm, bn, threads;
+    double one, two;
+};
+
+inline double f8_estimate(const F8GemmArgs& g, const F8Form& f, int64_t& tiles) {
+    tiles = ((int64_t)g.M + f.bm - 1) / f.bm * (((int64_t)g.N + f.bn - 1) / f.bn);
+    if (tiles * f.threads > 0xffffffffll) return 1e300;     // more threads than a launch holds
+    if (f.bm == 256) return f.one * (double)((tiles + 255) / 256);
+    return tiles <= 256 ? f.one : f.two * (double)((tiles + 511) / 512);
+}
+
 template <int AF, int BF, bool BTILES, bool EXACT> hipError_t f8_tiled(const F8GemmArgs& g, hipStream_t s) {
-    auto tiles = [&](int t) { return ((int64_t)g.M + t - 1) / t * (((int64_t)g.N + t - 1) / t); };
-    if (tiles(256) >= 192)
-        hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, EXACT, 256, 256, 128, 64>), dim3((unsigned)tiles(256)), dim3(512), 0, s, g);
-    else if (tiles(128) >= 160)
-        hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, EXACT, 128, 128, 64, 32>), dim3((unsigned)tiles(128)), dim3(512), 0, s, g);
-    else
-        hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, EXACT, 64, 64, 32, 32>), dim3((unsigned)tiles(64)), dim3(256), 0, s, g);
+    // the first form is the largest one, which holds every product that the entry point lets pass
+    constexpr int N = EXACT ? 3 : 4;
+    const F8Form fast[] = {{256, 256, 512, 1.87, 3.74}, {128, 128, 512, 0.75, 1.13}, {128, 64, 512, 0.42, 0.80}, {64, 64, 256, 0.40, 0.50}};
+    const F8Form exact[] = {{256, 128, 512, 1.90, 3.80}, {128, 64, 512, 0.69, 1.17}, {64, 64, 256, 0.60, 0.72}};
+    const F8Form* forms = EXACT ? exact : fast;
+    int best = 0;
+    int64_t tiles = 0;
+    double least = 1e301;
+    for (int i = 0; i < N; ++i) {
+        int64_t t;
+        const double e = f8_estimate(g, forms[i], t);
+        if (e < least) least = e, best = i, tiles = t;
+    }
+    const dim3 grid((unsigned)tiles), threads(forms[best].threads);
+    if constexpr (EXACT) {
+        if (best == 0) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, true, 256, 128, 64, 64, 2>), grid, threads, 0, s, g);
+        else if (best == 1) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, true, 128, 64, 32, 32, 3>), grid, threads, 0, s, g);
+        else hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, true, 64, 64, 32, 32, 3>), grid, threads, 0, s, g);
+    } else {
+        if (best == 0) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, false, 256, 256, 128, 64, 2>), grid, threads, 0, s, g);
+        else if (best == 1) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, false, 128, 128, 64, 32, 2>), grid, threads, 0, s, g);
+        else if (best == 2) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, false, 128, 64, 32, 32, 3>), grid, threads, 0, s, g);
+        else hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, false, 64, 64, 32, 32, 3>), grid, threads, 0, s, g);
+    }
     return hipGetLastError();
 }
 

@@ -654,7 +654,7 @@ BITOPT_API int bitopt_f8_dequantize(const uint8_t* codes, const float* scales, i
  * below it; with an fp32 result, and for up to 64 rows, on decoded elements, where products
  * are exact and sums are those of fp32.
  * Up to 64 rows of a take a form that reads b once.  k above 2^24 gives UNSUPPORTED, and so
- * do products that one launch does not hold: some 2^39 results, or 2^28 columns for up to
+ * do products that one launch does not hold: some 2^38 results, or 2^28 columns for up to
  * 64 rows.
  */
 BITOPT_API int bitopt_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t a_format,
