@@ -280,29 +280,183 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
     }
 }
 
+// ------------------------------------------------------- few tiles, a long contraction
+
+// As k_f8_gemm for products with fewer tiles than fill the chip, where a block of contraction
+// lasts as long as its loads: KS groups of waves share the tile, each taking every KS-th block, so
+// that KS blocks are loaded at once, NS - 1 such stages ahead.  The groups' sums meet in LDS, in
+// the order of the groups.
+template <int AF, int BF, bool BTILES, bool EXACT, int BM, int BN, int WM, int WN, int KS, int NS>
+__global__ __launch_bounds__(KS * (BM / WM) * (BN / WN) * 64) void k_f8_split(F8GemmArgs g) {
+    constexpr int WAVES = (BM / WM) * (BN / WN), NT = KS * WAVES * 64, FM = WM / 16, FN = WN / 16;
+    constexpr int BLOCK = (BM + BN) * 128, PASS_ROWS = NT / 8, PASSES = (BM + BN) / PASS_ROWS, LOADS = KS * PASSES;
+    constexpr int SR = BM + (BTILES ? 64 : BN);         // scales of a block: A's rows, then B's rows or tiles
+    constexpr int STAGE = KS * BLOCK + NT * 4;
+    static_assert(BM % PASS_ROWS == 0 && BN % PASS_ROWS == 0 && PASS_ROWS % 8 == 0, "whole passes per operand");
+    static_assert(KS * SR <= NT && kF8Block % WN == 0, "a scale for each thread at most; a wave's columns in one tile");
+    static_assert(KS * WAVES * FM * FN * 1024 <= NS * STAGE, "the sums fit where the codes were");
+    __shared__ __attribute__((aligned(16))) char lds[NS * STAGE];
+
+    int tm, tn;
+    mx_tile((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = wave / WAVES, part = wave % WAVES;
+    const int wm = part % (BM / WM) * WM, wn = part / (BM / WM) * WN;
+    const int q = lane >> 4, li = lane & 15;
+    const int steps = (int)f8_blocks(g.K), stages = (steps + KS - 1) / KS;
+
+    const int pr = tid >> 3, chunk = (tid & 7) ^ (pr & 7);
+    const uint8_t* a0 = g.a + (int64_t)m0 * g.row_bytes;
+    const uint8_t* b0 = g.b + (int64_t)n0 * g.row_bytes;
+    uint32_t off[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = i * PASS_ROWS + pr;
+        off[i] = (uint32_t)(i * PASS_ROWS < BM ? min(r, g.M - 1 - m0) : min(r - BM, g.N - 1 - n0)) * (uint32_t)g.row_bytes +
+                 chunk * 16;
+    }
+    // this thread's scale: of the stage's block sk, of A or B (a wave's are alike)
+    const int sk = min(wave * 64 / SR, KS - 1), sw = wave * 64 - sk * SR;
+    const bool of_a = sw < BM;
+    const int sr = (of_a ? sw : sw - BM) + lane;
+    const float* s0 = of_a ? g.a_scales + m0 : BTILES ? g.b_scales + (int64_t)(n0 / kF8Block) * steps : g.b_scales + n0;
+    const int64_t s_step = of_a ? g.M : BTILES ? 1 : g.N;
+    const uint32_t s_off = 4u * (of_a ? (uint32_t)min(sr, g.M - 1 - m0)
+                                      : BTILES ? (uint32_t)min(sr, (g.N - 1) / kF8Block - n0 / kF8Block) * (uint32_t)steps
+                                               : (uint32_t)min(sr, g.N - 1 - n0));
+    // blocks past the last repeat it, and are not read
+    auto issue = [&](int stage) {
+        char* to = lds + stage % NS * STAGE;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int64_t block = min(stage * KS + k, steps - 1);
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i)
+                load_to_lds<16>((i * PASS_ROWS < BM ? a0 : b0) + block * kF8Block, off[i], to + k * BLOCK + i * NT * 16 + wave * 1024);
+        }
+        load_to_lds<4>(s0 + min(stage * KS + sk, steps - 1) * s_step, s_off, to + KS * BLOCK + wave * 256);
+    };
+
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int lo = (q ^ (li & 7)) << 4, hi = ((q + 4) ^ (li & 7)) << 4;
+
+    for (int s = 0; s < NS - 1 && steps > 0; ++s) {
+        issue(s);
+        asm volatile("" ::: "memory");                  // in this order: the waits count on it
+    }
+    for (int s = 0; s < stages; ++s) {
+        // the stage is there, and every wave has read the one before, whose buffer is filled anew
+        f8_barrier<(NS - 2) * (LOADS + 1)>();
+        issue(s + NS - 1);
+        if (s * KS + group >= steps) continue;
+        const char* cur = lds + s % NS * STAGE + group * BLOCK;
+        const float* sc = reinterpret_cast<const float*>(lds + s % NS * STAGE + KS * BLOCK) + group * SR;
+        auto read = [&](int row, u32x4& x, u32x4& y) {
+            x = *reinterpret_cast<const u32x4*>(cur + (row + li) * 128 + lo);
+            y = *reinterpret_cast<const u32x4*>(cur + (row + li) * 128 + hi);
+        };
+        u32x4 ax[FM], ay[FM], bx[FN], by[FN];
+        float sa[FM];
+        f32x4 sb[BTILES ? 1 : FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) read(BM + wn + 16 * j, bx[j], by[j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) read(wm + 16 * i, ax[i], ay[i]);
+        if constexpr (BTILES) {
+            sb[0].x = sc[BM + wn / kF8Block];
+        } else {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(sc + BM + wn + 16 * j + 4 * q);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = sc[wm + 16 * i + li] * (BTILES ? sb[0].x : 1.0f);
+        u32x4 bh[EXACT ? FN : 1][4];
+        if constexpr (EXACT) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                bh[j][0] = f8_half8<BF>(bx[j].x, bx[j].y); bh[j][1] = f8_half8<BF>(bx[j].z, bx[j].w);
+                bh[j][2] = f8_half8<BF>(by[j].x, by[j].y); bh[j][3] = f8_half8<BF>(by[j].z, by[j].w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            f32x4 p[FN];
+            if constexpr (EXACT) {
+                const u32x4 ah[4] = {f8_half8<AF>(ax[i].x, ax[i].y), f8_half8<AF>(ax[i].z, ax[i].w),
+                                     f8_half8<AF>(ay[i].x, ay[i].y), f8_half8<AF>(ay[i].z, ay[i].w)};
+#pragma unroll
+                for (int j = 0; j < FN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) p[j] = mfma16<kBF16>(bh[j][h], ah[h], p[j]);
+            } else {
+                const i32x8 a = {(int)ax[i].x, (int)ax[i].y, (int)ax[i].z, (int)ax[i].w,
+                                 (int)ay[i].x, (int)ay[i].y, (int)ay[i].z, (int)ay[i].w};
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const i32x8 b = {(int)bx[j].x, (int)bx[j].y, (int)bx[j].z, (int)bx[j].w,
+                                     (int)by[j].x, (int)by[j].y, (int)by[j].z, (int)by[j].w};
+                    p[j] = mfma_f8<BF, AF>(b, a, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[j][r], BTILES ? sa[i] : sa[i] * sb[j][r], acc[i][j][r]);
+        }
+    }
+    f8_barrier<0>();                    // no load to LDS is under way, and every wave has read its last block
+    f32x4* sums = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sums[((group * WAVES + part) * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    // pair p of a wave's fragments is added up by group p % KS
+#pragma unroll
+    for (int p = 0; p < FM * FN / 2; ++p) {
+        if (p % KS != group) continue;
+        f32x4 v[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[h] += sums[((k * WAVES + part) * FM * FN + 2 * p + h) * 64 + lane];
+        const int i = 2 * p / FN, j = 2 * p % FN;
+        mx_store_pair(g, m0 + wm + 16 * i + li, n0 + wn + 16 * j, q, v[0], v[1]);
+    }
+}
+
 // ------------------------------------------------------------------------ tile choice
 
 // The form that is estimated to take the least time for a block of contraction: `one` us for up to 256
 // tiles (one a CU), else `two` for each 512; of the largest form one workgroup fills a CU.  Measured us of whole products with each form, 16-bit
 // results, B by tiles:
-//   M x N x K            256 x 256   128 x 128   128 x 64   64 x 64
+//   M x N x K            256 x 256   128 x 128   128 x 64   64 x 64   64 x 64, split
 //   8192 x 8192 x 2048   152         185         257        282
 //   8192 x 2048 x 8192   117         145         194        225
 //   4096 x 4096 x 4096   60          76          103        122
 //   2048 x 2048 x 2048               13.9        16.7       20.0
-//   1024 x 4096 x 4096   47          26.8        25.8       31.9
-//   1024 x 2048 x 8192   86          43          28.5       32.6
-//   512 x 2048 x 2048    27          10.7        8.3        7.5
-//   128 x 2048 x 8192    83          32          21.5       20.5
-//   777 x 1001 x 513                 7.1         5.5        4.6
+//   1024 x 4096 x 4096   47          26.8        25.8       31.9      39
+//   1024 x 2048 x 8192   86          43          28.5       32.6      38
+//   512 x 2048 x 2048    27          10.7        8.3        7.5       6.7
+//   128 x 2048 x 8192    83          32          21.5       20.3      15.2
+//   777 x 1001 x 513                 7.1         5.5        4.6       5.2
 // and with fp32 results, B by rows:
-//   M x N x K            256 x 128   128 x 64    64 x 64
+//   M x N x K            256 x 128   128 x 64    64 x 64    64 x 64, split
 //   8192 x 2048 x 8192   249         303         380
 //   4096 x 4096 x 4096   130         161         202
-//   1024 x 4096 x 4096   64          42          53
-//   1024 x 2048 x 8192   117         44          52
-//   512 x 2048 x 2048    34          13.5        11.8
-//   128 x 2048 x 8192    112         42          37
+//   1024 x 4096 x 4096   64          42          53         55
+//   1024 x 2048 x 8192   117         44          52         50
+//   512 x 2048 x 2048    34          13.5        11.8       9.3
+//   128 x 2048 x 8192    112         42          37         24.5
+//   777 x 1001 x 513                             6.2        6.3
+// The split form takes up to 256 small tiles whose contraction is eight blocks or more.
 struct F8Form {
     int bm, bn, threads;
     double one, two;
@@ -316,10 +470,11 @@ inline double f8_estimate(const F8GemmArgs& g, const F8Form& f, int64_t& tiles) 
 }
 
 template <int AF, int BF, bool BTILES, bool EXACT> hipError_t f8_tiled(const F8GemmArgs& g, hipStream_t s) {
-    // the first form is the largest one, which holds every product that the entry point lets pass
+    // the first form is the largest one: it holds every product that the entry point lets pass
     constexpr int N = EXACT ? 3 : 4;
-    const F8Form fast[] = {{256, 256, 512, 1.87, 3.74}, {128, 128, 512, 0.75, 1.13}, {128, 64, 512, 0.42, 0.80}, {64, 64, 256, 0.40, 0.50}};
-    const F8Form exact[] = {{256, 128, 512, 1.90, 3.80}, {128, 64, 512, 0.69, 1.17}, {64, 64, 256, 0.60, 0.72}};
+    const bool split = f8_blocks(g.K) >= 8;
+    const F8Form fast[] = {{256, 256, 512, 1.87, 0}, {128, 128, 512, 0.75, 1.13}, {128, 64, 512, 0.42, 0.80}, {64, 64, 256, split ? 0.24 : 0.40, 0.50}};
+    const F8Form exact[] = {{256, 128, 512, 1.90, 0}, {128, 64, 512, 0.69, 1.17}, {64, 64, 256, split ? 0.36 : 0.60, 0.72}};
     const F8Form* forms = EXACT ? exact : fast;
     int best = 0;
     int64_t tiles = 0;
@@ -330,7 +485,9 @@ template <int AF, int BF, bool BTILES, bool EXACT> hipError_t f8_tiled(const F8G
         if (e < least) least = e, best = i, tiles = t;
     }
     const dim3 grid((unsigned)tiles), threads(forms[best].threads);
-    if constexpr (EXACT) {
+    if (best == N - 1 && split && tiles <= 256)
+        hipLaunchKernelGGL((k_f8_split<AF, BF, BTILES, EXACT, 64, 64, 64, 32, 4, 2>), grid, dim3(512), 0, s, g);
+    else if constexpr (EXACT) {
         if (best == 0) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, true, 256, 128, 64, 64, 2>), grid, threads, 0, s, g);
         else if (best == 1) hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, true, 128, 64, 32, 32, 3>), grid, threads, 0, s, g);
         else hipLaunchKernelGGL((k_f8_gemm<AF, BF, BTILES, true, 64, 64, 32, 32, 3>), grid, threads, 0, s, g);

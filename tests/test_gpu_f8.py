@@ -153,10 +153,12 @@ def check(got, exact, bound, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()}, first at {bad.nonzero()[0].tolist()}, worst {float((off / bound).max())}"
 
 
-# few rows; tiles of 64, 128 and 256; one row, one column, less than a block, whole and ragged sizes
+# few rows; every form of tiles, also split over the contraction with 1 to 4 blocks in the last stage;
+# one row, one column, less than a block, whole and ragged sizes
 PRODUCTS = [(1, 1, 1), (1, 300, 128), (3, 17, 129), (16, 129, 640), (17, 64, 2048), (33, 400, 300), (64, 128, 1100),
             (65, 1, 1), (65, 65, 127), (128, 128, 128), (200, 333, 515), (64 + 1, 700, 1024), (1700, 1500, 256),
-            (1664, 1664, 384), (3584, 3584, 128), (3700, 3500, 300)]
+            (1664, 1664, 384), (3584, 3584, 128), (3700, 3500, 300), (1100, 1500, 300), (300, 500, 1025), (257, 100, 1290),
+            (70, 900, 1500), (512, 512, 2000)]
 
 
 @pytest.mark.parametrize("out", list(DT))
@@ -232,6 +234,21 @@ def test_products_without_a_contraction(m):
         y = torch.ones(m, 50, dtype=DT[out], device="cuda")
         bitopt.f8_matmul(*e8, *w8, 0, out=y, accumulate=True)
         assert (y == 1).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(70, 260, 2**23), (3, 140, 2**24)])
+def test_product_with_large_offsets(m, n, k):
+    """Rows of codes beyond 2^31 bytes: only elements near the ends of the last rows are not zero."""
+    a, b = torch.zeros(m, k, dtype=torch.uint8, device="cuda"), torch.zeros(n, k, dtype=torch.uint8, device="cuda")
+    sa, sb = torch.ones(k // 128, m, device="cuda"), torch.ones(k // 128, n, device="cuda")
+    sa[-1], sb[-2] = 2.0, 0.25
+    a[:, [5, k - 130, k - 1]], b[:, [5, k - 130, k - 1]] = 0x38, 0x40        # one, two
+    b[-1] = 0
+    b[-1, k - 1] = 0x30                                                       # a half
+    for out in ("f32", "bf16"):
+        y = bitopt.f8_matmul(a, sa, b, sb, k, dtype=DT[out])
+        # 2 + 2 / 4 + 2 * 2, and 2 / 2 in the last column
+        assert (y[:, :-1] == 6.5).all() and (y[:, -1] == 1.0).all()
 
 
 def test_scales_of_other_makers():
