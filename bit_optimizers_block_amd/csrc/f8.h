@@ -45,7 +45,7 @@ hipError_t launch_f8_dequantize(const F8CodecArgs& a, int dtype, int fmt, int bl
 // fast: on the 8-bit matrix instructions; exact: elements decoded to bf16 (every one is exact in it)
 hipError_t launch_f8_fast(const F8GemmArgs& g, int a_fmt, int b_fmt, int b_blocks, hipStream_t s);
 hipError_t launch_f8_exact(const F8GemmArgs& g, int a_fmt, int b_fmt, int b_blocks, hipStream_t s);
-constexpr int kF8FewRows = 64;
+constexpr int kF8FewRows = 32;
 hipError_t launch_f8_few(const F8GemmArgs& g, int a_fmt, int b_fmt, int b_blocks, hipStream_t s);
 
 #ifdef __HIPCC__

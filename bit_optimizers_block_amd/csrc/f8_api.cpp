@@ -92,8 +92,8 @@ int bitopt_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t a_fo
     BITOPT_TRY(check_dim(k, "k", fn));
     if (k > kMaxK) return api_fail(BITOPT_ERR_UNSUPPORTED, "%s: k above %lld", fn, (long long)kMaxK);
     if (m == 0 || n == 0) return api_status(hipSuccess, fn);
-    // a launch holds fewer than 2^32 threads: 512 for a tile of 256 x 128, 256 for 16 columns of few rows
-    const int64_t threads = m <= kF8FewRows ? (n + 15) / 16 * 256 : (m / 256 + 1) * (n / 128 + 1) * 512;
+    // a launch holds fewer than 2^32 threads: 512 for a tile of 256 x 128 or 16 columns of few rows
+    const int64_t threads = m <= kF8FewRows ? (n + 15) / 16 * 512 : (m / 256 + 1) * (n / 128 + 1) * 512;
     if (threads > 0xffffffffll)
         return api_fail(BITOPT_ERR_UNSUPPORTED, "%s: %lld x %lld results are too many for one launch", fn, (long long)m,
                         (long long)n);

@@ -1,4 +1,4 @@
-// F8 products with up to 64 rows of A (single tokens, small decoding batches).
+// F8 products with up to 32 rows of A (single tokens, small decoding batches).
 //
 // Bound by reading B once.  A workgroup takes 16 rows of B, and its waves take blocks of 128
 // contraction elements in turn: a wave's load covers 16 whole lines.  Codes are decoded to
@@ -10,7 +10,7 @@ namespace bitopt {
 
 template <int AF, int BF, bool BTILES, int MT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_f8_few(F8GemmArgs g) {
-    constexpr int U = MT == 1 ? 4 : 2;         // blocks of a wave in flight
+    constexpr int U = MT * WAVES == 4 ? 4 : 2;  // blocks of a wave in flight
     __shared__ f32x4 part[WAVES * MT * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
     const int n0 = (int)blockIdx.x * 16, blocks = (int)f8_blocks(g.K);
@@ -87,11 +87,16 @@ __global__ __launch_bounds__(WAVES * 64) void k_f8_few(F8GemmArgs g) {
 
 // ------------------------------------------------------------------------- launches
 
+// us with four and with eight waves, B by tiles: 1 x 50257 x 2048 20.5 to 22.3, 23.2; 1 x 2048 x 8192
+// 8.9, 7.1; 16 x 8192 x 8192 21.3, 19.7.  Beyond 32 rows the tiled forms are faster: 64 x 8192 x 2048
+// 13.1 and 8.1, 64 x 50257 x 2048 65 and 39 (17 x 4093 x 1999 5.6 and 7.2).
 template <int AF, int BF, bool BTILES> static hipError_t few(const F8GemmArgs& g, hipStream_t s) {
     const dim3 grid((unsigned)(((int64_t)g.N + 15) / 16));
-    if (g.M <= 16) hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 1, 4>), grid, dim3(256), 0, s, g);
-    else if (g.M <= 32) hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 2, 4>), grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 4, 4>), grid, dim3(256), 0, s, g);
+    const bool deep = f8_blocks(g.K) >= 32;
+    if (g.M <= 16 && deep) hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 1, 8>), grid, dim3(512), 0, s, g);
+    else if (g.M <= 16) hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 1, 4>), grid, dim3(256), 0, s, g);
+    else if (deep) hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 2, 8>), grid, dim3(512), 0, s, g);
+    else hipLaunchKernelGGL((k_f8_few<AF, BF, BTILES, 2, 4>), grid, dim3(256), 0, s, g);
     return hipGetLastError();
 }
 

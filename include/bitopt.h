@@ -649,13 +649,13 @@ BITOPT_API int bitopt_f8_dequantize(const uint8_t* codes, const float* scales, i
  * multiplied by its scales and added in fp32; the result is rounded once into out_dtype.  The
  * three products of a linear layer y = x W^T: x (rows) with W (tiles); dy (rows) with W^T
  * (tiles); dy^T (rows) with x^T (rows).
- * With a 16-bit result and more than 64 rows of a, a block's sum runs on the 8-bit matrix
+ * With a 16-bit result and more than 32 rows of a, a block's sum runs on the 8-bit matrix
  * instruction, which aligns the products to the largest one and drops what lies some 17 bits
- * below it; with an fp32 result, and for up to 64 rows, on decoded elements, where products
+ * below it; with an fp32 result, and for up to 32 rows, on decoded elements, where products
  * are exact and sums are those of fp32.
- * Up to 64 rows of a take a form that reads b once.  k above 2^24 gives UNSUPPORTED, and so
- * do products that one launch does not hold: some 2^38 results, or 2^28 columns for up to
- * 64 rows.
+ * Up to 32 rows of a take a form that reads b once.  k above 2^24 gives UNSUPPORTED, and so
+ * do products that one launch does not hold: some 2^38 results, or 2^27 columns for up to
+ * 32 rows.
  */
 BITOPT_API int bitopt_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t a_format,
                                 const uint8_t* b_codes, const float* b_scales, int32_t b_format, int32_t b_blocks,

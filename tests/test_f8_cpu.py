@@ -115,7 +115,7 @@ def test_refused(B, call, args, text):
 
 @pytest.mark.parametrize("call,args", [
     (quantize, dict(rows=2**30 + 1)), (dequantize, dict(cols=2**31)), (matmul, dict(k=2**24 + 1)),
-    (matmul, dict(m=2**29, n=2**29, ldo=2**29)), (matmul, dict(m=64, n=2**28, ldo=2**28)),
+    (matmul, dict(m=2**29, n=2**29, ldo=2**29)), (matmul, dict(m=32, n=2**27, ldo=2**27)),
     (matmul, dict(m=2**20, n=2**19, ldo=2**19)), (matmul, dict(m=2**31)),
 ])
 def test_unsupported(B, call, args):
