@@ -1,9 +1,10 @@
 // F8 codec: a matrix to 8 bits, itself, its transpose or both from one reading, and back.
 //
-// A workgroup takes a tile of 128 x 128 into registers, a lane 8 rows by 8 columns: sixteen
-// lanes side by side hold a row of the tile, so a row's maximum meets in DPP exchanges, and
-// a lane's eight rows are eight consecutive codes of the transpose, which go through LDS to
-// leave in whole lines.  Bound by HBM: the input is read once, the codes written once.
+// Bound by HBM: the input is read once, the codes written once.  Row blocks alone: a lane takes
+// eight elements, sixteen lanes make a block, whose maximum meets in DPP exchanges.  Tiles and
+// transposes: a workgroup takes a tile of 128 x 128 into registers, a lane 8 rows by 8 columns;
+// sixteen lanes side by side hold a row of the tile, and a lane's eight rows are eight consecutive
+// codes of the transpose, which go through LDS to leave in whole lines.
 #include "f8.h"
 #include "launch.h"
 #include "mx_rows.h"
@@ -16,6 +17,31 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));    // quad_perm 2,3,0,1
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));   // row_half_mirror
     return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, true));  // row_mirror
+}
+
+template <int DT, int FMT> __global__ __launch_bounds__(kThreads) void k_f8_rows(F8CodecArgs a, RowGrid g) {
+    const int64_t width = f8_padded(a.cols);
+    for_items(g, a.rows, (int32_t)(width / 8), [&](int64_t row, int32_t item) {
+        const int64_t c = 8 * (int64_t)item;
+        float v[8];
+        if (a.cols >= 8) {
+            Eight<DT> in;
+            in.template load<false>(a.x, row * a.ldx, c, a.cols);
+            in.values(c + 8 - a.cols, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = c + j < a.cols ? load1<DT>(a.x, row * a.ldx + c + j) : 0.0f;
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        const F8Scale f = f8_scale<FMT>(max16(m));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f8_scaled<DT>(v[j], f.r);
+        const u32x2 codes = {f8_encode4<FMT>(v[0], v[1], v[2], v[3]), f8_encode4<FMT>(v[4], v[5], v[6], v[7])};
+        *gbl(reinterpret_cast<u32x2*>(a.codes + row * width + c)) = f.r == 0.0f ? u32x2{0u, 0u} : codes;
+        if (item % 16 == 0) gbl(a.scales)[item / 16 * a.rows + row] = f.s;
+    });
 }
 
 template <int DT, int FMT, bool TILES, bool T> __global__ __launch_bounds__(kThreads) void k_f8_quantize(F8CodecArgs a) {
@@ -157,7 +183,11 @@ template <int DT, int FMT> static hipError_t quantize(const F8CodecArgs& a, bool
     if (tiles && a.codes_t) hipLaunchKernelGGL((k_f8_quantize<DT, FMT, true, true>), grid, dim3(kThreads), 0, s, a);
     else if (tiles) hipLaunchKernelGGL((k_f8_quantize<DT, FMT, true, false>), grid, dim3(kThreads), 0, s, a);
     else if (a.codes_t) hipLaunchKernelGGL((k_f8_quantize<DT, FMT, false, true>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_f8_quantize<DT, FMT, false, false>), grid, dim3(kThreads), 0, s, a);
+    else {
+        dim3 over;
+        const RowGrid g = row_grid(a.rows, f8_padded(a.cols) / 8, over);
+        hipLaunchKernelGGL((k_f8_rows<DT, FMT>), over, dim3(kThreads), 0, s, a, g);
+    }
     return hipGetLastError();
 }
 

@@ -28,7 +28,7 @@ def kernels():
     return found
 
 
-@pytest.mark.parametrize("family", ["k_f8_gemm", "k_f8_split", "k_f8_few", "k_f8_quantize", "k_f8_dequantize", "k_dropout",
+@pytest.mark.parametrize("family", ["k_f8_gemm", "k_f8_split", "k_f8_few", "k_f8_rows", "k_f8_quantize", "k_f8_dequantize", "k_dropout",
                                     "k_embedding_sort", "k_embedding_sums", "k_embedding_join", "k_embedding_count",
                                     "k_embedding_scan", "k_embedding_move", "11k_embedding", "k_mx_embedding"])
 def test_no_scratch(kernels, family):

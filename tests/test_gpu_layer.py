@@ -226,7 +226,7 @@ def test_embedding_large_offsets():
 # counts on both sides of one workgroup's sort at each of its sizes, and of a part's length
 GRADS = [(1, 1, 1), (1, 50257, 9), (33, 7, 8), (700, 300, 130), (1024, 2**18, 33), (1025, 5000, 77), (4096, 4096, 40),
          (4097, 255, 256), (8193, 256, 16), (16384, 65535, 24), (16385, 65536, 24), (20000, 3, 513), (70000, 2**20, 5),
-         (40, 2**27, 1)]
+         (40, 2**27, 1), (1100000, 700, 9)]
 
 
 @pytest.mark.parametrize("kind", ["any", "one", "often", "padded", "outside", "few"])
