@@ -313,19 +313,20 @@ __global__ __launch_bounds__(kThreads) void k_embedding_sums(EmbeddingGradArgs a
         bool begins = first == 0 || gbl(keys)[first - 1] != run;
         float sum[8] = {};
         for (int64_t i = first; i < end && run < none; i += U) {
-            uint32_t key[U + 1];
+            uint32_t key[U + 1], from[U];
             float v[U][8], old[ADD ? U : 1][8];
 #pragma unroll
             for (int k = 0; k <= U; ++k) {
                 const uint32_t at = gbl(keys)[min(i + k, a.count - 1)];
                 key[k] = i + k < a.count ? at : none;
+                if (k < U) from[k] = gbl(order)[min(i + k, end - 1)];
             }
             if (a.width >= 8) {
                 Eight<DT> in[U];
                 Eight<OUT> was[ADD ? U : 1];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    in[k].template load<false>(a.dy, (int64_t)gbl(order)[min(i + k, end - 1)] * a.lddy, e, a.width);
+                    in[k].template load<false>(a.dy, (int64_t)from[k] * a.lddy, e, a.width);
                     if constexpr (ADD) was[k].template load<false>(a.out, (key[k] < none ? key[k] : 0) * a.ldo, e, a.width);
                 }
 #pragma unroll
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(kThreads) void k_embedding_sums(EmbeddingGradArgs a
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const bool in = j < a.width;
-                        v[k][j] = in ? load1<DT>(a.dy, (int64_t)gbl(order)[min(i + k, end - 1)] * a.lddy + j) : 0.0f;
+                        v[k][j] = in ? load1<DT>(a.dy, (int64_t)from[k] * a.lddy + j) : 0.0f;
                         if constexpr (ADD) old[k][j] = in ? load1<OUT>(a.out, (key[k] < none ? key[k] : 0) * a.ldo + j) : 0.0f;
                     }
             }
