@@ -4,7 +4,10 @@
 // eight elements, sixteen lanes make a block, whose maximum meets in DPP exchanges.  Tiles and
 // transposes: a workgroup takes a tile of 128 x 128 into registers, a lane 8 rows by 8 columns;
 // sixteen lanes side by side hold a row of the tile, and a lane's eight rows are eight consecutive
-// codes of the transpose, which go through LDS to leave in whole lines.
+// codes of the transpose, which go through LDS to leave in whole lines.  Measured: 8192 x 2048 bf16 by
+// rows 10.7 us, 8192 x 8192 bf16 by rows with the transpose 49 (5.2 TB/s), 8192 x 2048 fp32 by tiles
+// with the transpose 22.9 (4.4 TB/s); back to fp32 12.4 (6.8 TB/s, part of it from the last-level
+// cache).
 #include "f8.h"
 #include "launch.h"
 #include "mx_rows.h"

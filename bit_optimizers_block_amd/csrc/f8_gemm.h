@@ -55,6 +55,18 @@ template <int SIZE> __device__ __forceinline__ void load_to_lds(const void* base
 // ahead of the last two groups, which go column by column, so that B's fragments are free one after
 // the other for the reads of the next block.  Exact: ahead of the last group; B's decoded fragments
 // leave no registers for the next ones.
+//
+// Bound: the SIMD's instructions.  Matrix and vector instructions of its two waves do not overlap:
+// at 8192 x 2048 x 8192, fast, B by tiles (110 to 117 us, 2350 to 2500 TFLOP/s), the matrix pipes are
+// busy 57% of the cycles and other vector instructions, nearly all of them the 128 additions of a
+// block, another 34%; with the additions left out it takes 101.  LDS is busy 25%, without
+// conflicts.  By rows each addition takes a product of two scales besides (125 to 130 us), and in the
+// exact form the decoding (250).  Where the contraction is short the results' stores show:
+// 8192 x 8192 x 2048 takes 150 to 155 us, some 30 of them 134 MB of results that nothing overlaps (one
+// workgroup a CU; a resident grid whose next tile's loads go ahead of the stores spilled).
+// Earlier forms: a fragment's reads waited for right ahead of its products, and the loads of the next
+// block with a tile's scale, 168 us; the barrier ahead of the last group only, 124.  A wave's
+// priority raised for half of the waves: 114 to 117.  128 x 128 tiles on four waves: 146.
 template <int AF, int BF, bool BTILES, bool EXACT, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmArgs g) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64, FM = WM / 16, FN = WN / 16;

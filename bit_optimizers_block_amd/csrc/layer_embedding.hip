@@ -6,6 +6,13 @@
 // cut into windows of `span` places, each added up by one group of lanes with eight rows in
 // flight, whatever the runs' lengths; a run that lies in several windows (a frequent token)
 // leaves its parts in the workspace, and a second kernel adds those in their order.
+//
+// Measured, 8192 bf16 rows of 2048 into 50257 fp32 rows: 95 us, of which 65 clear the table (6.3 TB/s;
+// the sort, 17.6 by itself, runs beside that), 22 are the sums and 7 the parts; added to what is
+// there 46.  The sums wait for three loads in turn (places, rows, the table's rows where added) and
+// find the memory still busy with the cleared rows.  Clearing only 64 MB beside the sort and the
+// rest, less the rows with a token, beside the sums: 128 us of a pass with the lookup against 121.
+// Streamed stores of the zeros: 128 against 124.  The lookup (100 MB) takes 12.5 us.
 #include "launch.h"
 #include "layer.h"
 #include "mx_rows.h"
