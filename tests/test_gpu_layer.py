@@ -407,3 +407,61 @@ def test_training_step():
             bitopt.step_8bit_blockwise_2state(hp, step, p.view(-1), g.contiguous().view(-1), s1, s2, a1, a2, q1, q2)
             moved = (p - before).abs().max()
             assert torch.isfinite(p).all() and 0 < float(moved) < 0.1
+
+
+@pytest.mark.parametrize("given", ["own", "default"])
+def test_streams_of_other_libraries(monkeypatch, given):
+    """Any object with a stream's handle: the work of every call goes to that very stream."""
+    x, table = values(1, 70, 130, "bf16"), values(2, 90, 130, "f32")
+    tokens = torch.from_numpy(tokens_of("padded", 70, 90)).cuda()
+    q = bitopt.f8_quantize(x, give="both")
+    w, mx = bitopt.f8_quantize(table, blocks="tiles"), bitopt.mx_quantize(table)
+
+    def calls(**stream):
+        return [*bitopt.f8_quantize(x, give="both", **stream), bitopt.f8_dequantize(*q[:2], 130, **stream),
+                bitopt.f8_matmul(*q[:2], *w, 130, b_blocks="tiles", **stream), bitopt.dropout(x, 0.3, 1, residual=x, **stream),
+                bitopt.dropout_backward(x, 0.3, 1, **stream), bitopt.embedding(tokens, table, **stream),
+                bitopt.mx_embedding(tokens, *mx, 130, **stream), bitopt.embedding_backward(x, tokens, 90, **stream)]
+    want = calls()
+    torch.cuda.synchronize()
+    own = torch.cuda.Stream() if given == "own" else torch.cuda.default_stream()
+    handle, seen, real = type("Handle", (), dict(cuda_stream=own.cuda_stream))(), [], bitopt.lib()
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                seen.append(args[-1])
+                return getattr(real, name)(*args)
+            return getattr(real, name) if name.endswith("bytes") or name == "bitopt_last_error" else call
+    monkeypatch.setattr(bitopt, "lib", Library)
+    with torch.cuda.stream(torch.cuda.Stream()):        # neither the given stream nor the default one
+        got = calls(stream=handle)
+    torch.cuda.synchronize()
+    assert seen == [own.cuda_stream] * 8
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_results_have_no_history():
+    """Arguments that require a gradient are taken, and their results require none; the gradient calls
+    serve a torch.autograd.Function."""
+    table = torch.nn.Parameter(values(1, 60, 40, "f32"))
+    tokens = torch.from_numpy(tokens_of("padded", 100, 60)).cuda()
+
+    class Embedding(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, table, call):
+            ctx.call, ctx.vocab = call, table.shape[0]
+            return bitopt.dropout(bitopt.embedding(tokens, table, 2.0), 0.25, 9, call)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return bitopt.embedding_backward(bitopt.dropout_backward(dy, 0.25, 9, ctx.call), tokens, ctx.vocab, 2.0), None
+    y = bitopt.dropout(bitopt.embedding(tokens, table, 2.0), 0.25, 9, 3)
+    assert not y.requires_grad and y.grad_fn is None
+    got = Embedding.apply(table, 3)
+    assert torch.equal(got, y)
+    dy = values(2, 100, 40, "f32")
+    got.backward(dy)
+    assert torch.equal(table.grad, bitopt.embedding_backward(bitopt.dropout_backward(dy, 0.25, 9, 3), tokens, 60, 2.0))
+    for t in bitopt.f8_quantize(table, give="both"):
+        assert not t.requires_grad and t.grad_fn is None
