@@ -865,29 +865,33 @@ def _f8_blocks(blocks):
 
 def _f8_operand(codes, scales, cols, blocks, name, device):
     """Checks an F8 matrix of `cols` columns; returns its rows."""
+    kb = (cols + 127) // 128
+    if codes.dim() == 2:
+        rows, width = codes.shape
+        if width == kb * 128 and scales.shape == ((-(-rows // 128), kb) if blocks else (kb, rows)) and \
+                codes.dtype is torch.uint8 and scales.dtype is torch.float32 and codes.is_contiguous() and \
+                scales.is_contiguous() and codes.is_cuda and codes.device == device and scales.device == device:
+            return rows
     if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
         raise TypeError(f"{name}: expected torch.uint8 codes and torch.float32 scales, got {codes.dtype}, {scales.dtype}")
-    kb = (cols + 127) // 128
     rows = codes.size(0) if codes.dim() == 2 else -1
     if codes.shape != (rows, kb * 128) or not codes.is_contiguous():
         raise ValueError(f"{name} codes: expected a contiguous matrix of {kb * 128} bytes a row for {cols} columns, got "
                          f"shape {tuple(codes.shape)}")
-    shape = ((rows + 127) // 128, kb) if blocks else (kb, rows)
+    shape = (-(-rows // 128), kb) if blocks else (kb, rows)
     if scales.shape != shape or not scales.is_contiguous():
         raise ValueError(f"{name} scales: expected a contiguous matrix of shape {shape} for {rows} x {cols} elements, got "
                          f"{tuple(scales.shape)}")
     if not codes.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if codes.device != device or scales.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return rows
+    raise ValueError(f"{name} must be on {device}")
 
 
 def _f8_new(rows, cols, blocks, device):
     kb = (cols + 127) // 128
-    shape = ((rows + 127) // 128, kb) if blocks else (kb, rows)
+    r, c = (-(-rows // 128), kb) if blocks else (kb, rows)
     return (torch.empty_strided((rows, kb * 128), (kb * 128, 1), dtype=torch.uint8, device=device),
-            torch.empty_strided(shape, (shape[1], 1), dtype=torch.float32, device=device))
+            torch.empty_strided((r, c), (c, 1), dtype=torch.float32, device=device))
 
 
 def f8_quantize(x, fmt: str = "e4m3", blocks: str = "rows", give: str = "rows", out=None, stream=None):
@@ -896,13 +900,16 @@ def f8_quantize(x, fmt: str = "e4m3", blocks: str = "rows", give: str = "rows", 
     out: the caller's tensors for the result, in that order."""
     rows, cols, ldx = _rows(x, "x")
     dt, device = _dt(x), x.device
-    f, b = _f8_format(fmt), _f8_blocks(blocks)
-    if give not in ("rows", "columns", "both"):
+    f, b = F8_FORMATS.get(fmt), F8_BLOCKS.get(blocks)
+    if f is None or b is None:
+        _f8_format(fmt), _f8_blocks(blocks)
+    if give != "rows" and give != "both" and give != "columns":
         raise ValueError(f"give must be 'rows', 'columns' or 'both', got {give!r}")
     other = _elsewhere(device, stream)
     if other is not None:
         with other:
             return f8_quantize(x, fmt, blocks, give, out)
+    c = s = ct = st = None
     if out is None:
         out = () if give == "columns" else _f8_new(rows, cols, b, device)
         if give != "rows":
@@ -911,13 +918,14 @@ def f8_quantize(x, fmt: str = "e4m3", blocks: str = "rows", give: str = "rows", 
         out = tuple(out)
         if len(out) != (4 if give == "both" else 2):
             raise ValueError(f"out: expected {4 if give == 'both' else 2} tensors, got {len(out)}")
-        if give != "columns" and _f8_operand(*out[:2], cols, b, "the result", device) != rows:
+        if give != "columns" and _f8_operand(out[0], out[1], cols, b, "the result", device) != rows:
             raise ValueError(f"the result: expected {rows} rows of codes, got {out[0].size(0)}")
-        if give != "rows" and _f8_operand(*out[-2:], rows, b, "the transposed result", device) != cols:
+        if give != "rows" and _f8_operand(out[-2], out[-1], rows, b, "the transposed result", device) != cols:
             raise ValueError(f"the transposed result: expected {cols} rows of codes, got {out[-2].size(0)}")
-    p = [t.data_ptr() for t in out]
-    c, s = (None, None) if give == "columns" else p[:2]
-    ct, st = (None, None) if give == "rows" else p[-2:]
+    if give != "columns":
+        c, s = out[0].data_ptr(), out[1].data_ptr()
+    if give != "rows":
+        ct, st = out[-2].data_ptr(), out[-1].data_ptr()
     _check(lib().bitopt_f8_quantize(x.data_ptr(), dt, rows, cols, ldx, f, b, c, s, ct, st, _current(device)))
     return out
 
@@ -926,7 +934,9 @@ def f8_dequantize(codes, scales, cols: int, fmt: str = "e4m3", blocks: str = "ro
                   stream=None):
     """The values of an F8 matrix of `cols` columns."""
     device = codes.device
-    f, b = _f8_format(fmt), _f8_blocks(blocks)
+    f, b = F8_FORMATS.get(fmt), F8_BLOCKS.get(blocks)
+    if f is None or b is None:
+        _f8_format(fmt), _f8_blocks(blocks)
     rows = _f8_operand(codes, scales, cols, b, "the input", device)
     other = _elsewhere(device, stream)
     if other is not None:
@@ -943,7 +953,9 @@ def f8_matmul(a_codes, a_scales, b_codes, b_scales, k: int, a_fmt: str = "e4m3",
     """a b^T for F8 matrices a (m x k, by rows) and b (n x k, by rows or tiles); `accumulate`
     adds it to `out`."""
     device = a_codes.device
-    fa, fb, b = _f8_format(a_fmt), _f8_format(b_fmt), _f8_blocks(b_blocks)
+    fa, fb, b = F8_FORMATS.get(a_fmt), F8_FORMATS.get(b_fmt), F8_BLOCKS.get(b_blocks)
+    if fa is None or fb is None or b is None:
+        _f8_format(a_fmt), _f8_format(b_fmt), _f8_blocks(b_blocks)
     m = _f8_operand(a_codes, a_scales, k, 0, "a", device)
     n = _f8_operand(b_codes, b_scales, k, b, "b", device)
     if accumulate and out is None:
