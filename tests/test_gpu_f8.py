@@ -175,9 +175,10 @@ def test_product(m, n, k, af, bf, blocks, out):
 
 
 @pytest.mark.parametrize("out", list(DT))
+@pytest.mark.parametrize("k", [300, 1100])
 @pytest.mark.parametrize("m", [5, 20, 130])
-def test_product_accumulates_into_strided_rows(m, out):
-    n, k = 77, 300
+def test_product_accumulates_into_strided_rows(m, k, out):
+    n = 77
     a, b = matrix(1, m, k, "e5m2"), matrix(2, n, k, "e4m3")
     old = values(3, m, n, out)
     y = padded_rows(old, 5, 1, fill=99.0)
@@ -193,11 +194,12 @@ def test_product_accumulates_into_strided_rows(m, out):
     check(y, exact, R.product_bound(a[2], b[2], exact, out, m > 32 and out != "f32"))
 
 
+@pytest.mark.parametrize("k", [400, 1300])
 @pytest.mark.parametrize("m", [5, 130])
 @pytest.mark.parametrize("blocks", ["rows", "tiles"])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_non_finite_blocks_stay_in_their_rows(m, blocks, out):
-    n, k = 300, 400
+def test_non_finite_blocks_stay_in_their_rows(m, k, blocks, out):
+    n = 300
     a, b = matrix(1, m, k, "e4m3"), matrix(2, n, k, "e4m3", blocks)
     a[1][1, 3] = float("nan")
     b[1][0, 140 if blocks == "rows" else 1] = float("nan")
