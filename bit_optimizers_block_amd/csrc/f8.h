@@ -108,19 +108,207 @@ template <int FMT> __device__ __forceinline__ void f8_decode4(uint32_t c, float 
     v[0] = p.x; v[1] = p.y; v[2] = q.x; v[3] = q.y;
 }
 
-// Eight codes -> bf16, exact: four or three significant bits, exponents from -16 to 15.
-template <int FMT> __device__ __forceinline__ u32x4 f8_half8(uint32_t lo, uint32_t hi) {
+// Scales of any size.  The loops multiply a block's sum p by the product of its two scales, which may leave
+// fp32's range where p sa sb does not.  Where sa sb overflows, the result is infinite or NaN.  Where it
+// is below the normal numbers, a block is off by |p| 2^-150 at most, so the results not below 2^24 times the sum of
+// that over all blocks (f8_least) are right.  Of the others those are right whose row of A or row of B is all
+// zero.  Where one is left, its tile is taken once more with every scale as f s: f, a power of two, goes into p
+// by way of the elements or of the matrix instruction, and the product of two s stays in range.  Results
+// that were right keep their bits in that.
+// Measured, bf16 results: 8192 x 8192 x 2048 131.5 -> 134.1 us, 8192 x 2048 x 8192 112.1 -> 112.2; with 2% of A's rows
+// zero 131.6 -> 141.2, 110.3 -> 112.2.  Inside the loops it costs more: every scale taken apart 114 -> 119 (B by rows
+// 130 -> 147, fp32 results 250 -> 274), a branch to that where a block needs it spills.
+template <int AF, int BF> __device__ __forceinline__ float f8_least(int blocks) {
+    return (float)blocks * (float)(kF8Block * 0x1p-126 * kF8Top<AF> * kF8Top<BF>);
+}
+__device__ __forceinline__ bool f8_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
+
+// Of the rows of codes whose bits are set, those that hold a code which is neither 0 nor -0; by a whole wave.
+__device__ __forceinline__ uint64_t f8_hold(const uint8_t* codes, int64_t bytes, uint64_t rows) {
+    uint64_t held = 0;
+    for (; rows; rows &= rows - 1) {
+        const uint8_t* row = codes + __builtin_ctzll(rows) * bytes;
+        uint32_t any = 0;
+        for (int64_t c = 16 * (threadIdx.x & 63); c < bytes; c += 4096)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const u32x4 w = *gbl(reinterpret_cast<const u32x4*>(row + min(c + 1024 * k, bytes - 16)));
+                any |= w.x | w.y | w.z | w.w;
+            }
+        if (f8_any((any & 0x7f7f7f7fu) != 0)) held |= rows & -rows;
+    }
+    return held;
+}
+
+// Of a wave's 16 R x 16 C results, a lane's four consecutive columns of a row in each tile of 16: the
+// smallest of the lane's rows, and whether one is infinite or NaN.  Rows and columns beyond the matrix
+// repeat its last ones.
+template <int R, int C> __device__ __forceinline__ bool f8_lows(const f32x4 (&v)[R][C], float low[R]) {
+    float high = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        low[i] = __builtin_inff();
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                low[i] = __builtin_elementwise_minimum(low[i], fabsf(v[i][j][r]));     // NaN where there is one
+                high = __builtin_elementwise_maximum(high, fabsf(v[i][j][r]));
+            }
+    }
+    return f8_any(!(high < __builtin_inff()));
+}
+
+// The rows of 16 with a lane that says so.
+__device__ __forceinline__ uint64_t f8_rows_with(bool v) {
+    const uint64_t in = __builtin_amdgcn_ballot_w64(v);
+    return (in | in >> 16 | in >> 32 | in >> 48) & 0xffff;
+}
+
+// Whether a column from n on holds a code where a result of the rows that are left is below `least`.
+template <int R, int C>
+__device__ __forceinline__ bool f8_columns(const F8GemmArgs& g, const f32x4 (&v)[R][C], const bool row[R], int n, float least) {
+    const int q = (threadIdx.x & 63) >> 4;
+    uint64_t cols = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            bool small = false;
+#pragma unroll
+            for (int i = 0; i < R; ++i) small |= row[i] && fabsf(v[i][j][r]) < least;
+            const uint64_t in = __builtin_amdgcn_ballot_w64(small && n + 16 * j + 4 * q + r < g.N);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) cols |= (uint64_t)((in >> 16 * k & 0xffff) != 0) << (16 * j + 4 * k + r);
+        }
+    return f8_hold(g.b + (int64_t)n * g.row_bytes, g.row_bytes, cols) != 0;
+}
+
+// Whether a workgroup's results have to be taken once more, those of this wave v, from row m0 + wm and column n.
+// words: F8Words<BM, WAVES>::count of LDS.
+template <int BM, int WAVES> struct F8Words {
+    static constexpr int rows = (BM + 63) / 64, each = rows + 1, count = 2 * WAVES * each + WAVES;
+    static_assert(WAVES * each <= 64, "a word for each lane");
+};
+template <int BM, int WAVES, int R, int C>
+__device__ __forceinline__ bool f8_again(const F8GemmArgs& g, const f32x4 (&v)[R][C], int m0, int wm, int n, float least,
+                                         uint64_t* words) {
+    constexpr int W = F8Words<BM, WAVES>::rows, E = F8Words<BM, WAVES>::each;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15;
+    float low[R];
+    const bool bad = f8_lows(v, low);
+    uint64_t mine[W] = {};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const uint64_t rows = f8_rows_with(low[i] < least && m0 + wm + 16 * i + li < g.M);
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            if ((wm + 16 * i) / 64 == w) mine[w] |= rows << (wm + 16 * i) % 64;
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) words[wave * E + w] = mine[w];
+        words[wave * E + W] = bad;
+    }
+    __syncthreads();
+    const uint64_t word = lane < WAVES * E ? words[lane] : 0;
+    const bool set = word != 0;
+    if (__builtin_expect(!f8_any(set), 1)) return false;
+    if (f8_any(set && lane % E == W)) return true;
+    // rows that hold a code, each looked at by one wave
+    uint64_t* held = words + WAVES * E;
+    int turn = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        uint64_t rows = 0;
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k)
+            rows |= (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)word, k * E + w) |
+                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(word >> 32), k * E + w) << 32;
+        uint64_t own = 0;
+        for (; rows; rows &= rows - 1)
+            if (turn++ % WAVES == wave) own |= rows & -rows;
+        const uint64_t found = f8_hold(g.a + (int64_t)(m0 + 64 * w) * g.row_bytes, g.row_bytes, own);
+        if (lane == 0) held[wave * W + w] = found;
+    }
+    __syncthreads();
+    if (!f8_any(lane < WAVES * W && held[lane] != 0)) return false;
+    // in those rows, columns that hold one
+    bool row[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        uint64_t found = 0;
+        for (int k = 0; k < WAVES; ++k) found |= held[k * W + (wm + 16 * i) / 64];
+        row[i] = found >> ((wm + 16 * i) % 64 + li) & 1;
+    }
+    uint64_t* again = held + WAVES * E;
+    const bool yes = f8_columns(g, v, row, n, least);
+    if (lane == 0) again[wave] = yes;
+    __syncthreads();
+    return f8_any(lane < WAVES && again[lane] != 0);
+}
+
+// The same of 16 x 16 results that one wave has.
+__device__ __forceinline__ bool f8_again(const F8GemmArgs& g, const f32x4 (&v)[1][1], int m, int n, float least) {
+    const int li = threadIdx.x & 15;
+    float low[1];
+    if (f8_lows(v, low)) return true;
+    const uint64_t rows = f8_rows_with(low[0] < least && m + li < g.M);
+    if (__builtin_expect(rows == 0, 1)) return false;
+    const uint64_t found = f8_hold(g.a + (int64_t)m * g.row_bytes, g.row_bytes, rows);
+    const bool row[1] = {(found >> li & 1) != 0};
+    return found && f8_columns(g, v, row, n, least);
+}
+
+// Results go out before they are looked at, which then runs beside the stores (ahead of them: 136.1 us for the
+// 134.1 above), and once more where they were taken once more.  Results to be added to old ones wait.
+template <class Store, class Again, class Redo>
+__device__ __forceinline__ void f8_store(bool accumulate, bool look, Store store, Again again, Redo redo) {
+    if (!accumulate) store();
+    const bool more = look && again();
+    if (more) redo();
+    if (accumulate || more) store();
+}
+
+// A scale as f s for elements that are decoded, which bf16 has to hold with f:
+//   |scale|              f        |s|
+//   below 2^-63          2^-63    below 1
+//   below 2^64           1        from 2^-63 to 2^64
+//   the others           2^64     from 1 to 2^64
+// No product of two s reaches 2^128, and one below 2^-126 has a result below 2^-150.  A product of
+// two elements times fa fb leaves fp32's range only where that of the elements and their scales does.
+struct F8Fold {
+    float f, s;
+};
+__device__ __forceinline__ F8Fold f8_fold(float scale) {
+    const float a = fabsf(scale), f = a < 0x1p-63f ? 0x1p-63f : a < 0x1p64f ? 1.0f : 0x1p64f;
+    return {f, scale * __uint_as_float(0x7f000000u - __float_as_uint(f))};      // of a NaN, s is NaN
+}
+
+// The same for the 8-bit matrix instruction, which takes the byte e of 2^(e - 127) for each row: all of the
+// exponent, s from 1 to 2 (below where the scale is subnormal).  e = 255 of a NaN makes the result one.
+struct F8Parts {
+    int e;
+    float s;
+};
+__device__ __forceinline__ F8Parts f8_parts(float scale) {
+    const int e = (int)(__float_as_uint(scale) >> 23 & 255u);
+    return {e, __builtin_amdgcn_ldexpf(scale, 127 - e)};
+}
+
+// Eight codes times f -> bf16, exact: four or three significant bits, exponents from -16 to 15 and f's.
+template <int FMT> __device__ __forceinline__ u32x4 f8_half8(uint32_t lo, uint32_t hi, float f = 1.0f) {
     u32x4 r;
     if constexpr (FMT == kF8E4M3) {
-        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
-        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
-        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
-        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true));
     } else {
-        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false));
-        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true));
-        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false));
-        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true));
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, f, false));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, f, true));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, f, false));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, f, true));
     }
     return r;
 }

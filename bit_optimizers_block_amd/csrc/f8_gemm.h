@@ -20,6 +20,30 @@ template <int AF, int BF> __device__ __forceinline__ f32x4 mfma_f8(i32x8 a, i32x
     // scale operands of zero select the instruction without scales
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, AF, BF, 0, 0, 0, 0);
 }
+// The same times 2^(ea - 127) for a lane's row of A and 2^(eb - 127) for its row of B.
+template <int AF, int BF> __device__ __forceinline__ f32x4 mfma_f8(i32x8 a, i32x8 b, f32x4 c, int ea, int eb) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, AF, BF, 0, ea, 0, eb);
+}
+
+// A scale taken apart: what goes into the products of a lane's row, and the rest of it.
+template <bool EXACT> using F8Factor = std::conditional_t<EXACT, float, int>;
+template <bool EXACT> __device__ __forceinline__ F8Factor<EXACT> f8_take(float scale, float& rest) {
+    if constexpr (EXACT) {
+        const F8Fold v = f8_fold(scale);
+        rest = v.s;
+        return v.f;
+    } else {
+        const F8Parts v = f8_parts(scale);
+        rest = v.s;
+        return v.e;
+    }
+}
+template <bool EXACT> __device__ __forceinline__ f32x4 f8_rest(f32x4 scale) {
+    float r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f8_take<EXACT>(scale[i], r[i]);
+    return f32x4{r[0], r[1], r[2], r[3]};
+}
 
 // Waits until at most N of the wave's global loads are outstanding and its LDS reads are done, then
 // for the workgroup.  The empty statements keep memory accesses on their side.
@@ -87,8 +111,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
     // this lane's part of pass i, from the tile's first byte of a block: rows beyond the matrix
     // repeat its last row
     const int pr = tid >> 3, chunk = (tid & 7) ^ (pr & 7);
-    const uint8_t* a_next = g.a + (int64_t)m0 * g.row_bytes;
-    const uint8_t* b_next = g.b + (int64_t)n0 * g.row_bytes;
+    const uint8_t *a_next, *b_next;
     uint32_t off[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -99,11 +122,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
     // this thread's scale of a block (a wave's are all A's or all B's), and how far the next block's is
     const bool of_a = wave * 64 < BM;
     const int sr = of_a ? tid : tid - BM;
-    const float* s_next = of_a ? g.a_scales + m0 : BTILES ? g.b_scales + (int64_t)(n0 / kF8Block) * steps : g.b_scales + n0;
+    const float* s_next;
     const int64_t s_step = of_a ? g.M : BTILES ? 1 : g.N;
     const uint32_t s_off = 4u * (of_a ? (uint32_t)min(sr, g.M - 1 - m0)
                                       : BTILES ? (uint32_t)min(sr, (g.N - 1) / kF8Block - n0 / kF8Block) * (uint32_t)steps
                                                : (uint32_t)min(sr, g.N - 1 - n0));
+    auto begin = [&] {
+        a_next = g.a + (int64_t)m0 * g.row_bytes;
+        b_next = g.b + (int64_t)n0 * g.row_bytes;
+        s_next = of_a ? g.a_scales + m0 : BTILES ? g.b_scales + (int64_t)(n0 / kF8Block) * steps : g.b_scales + n0;
+    };
     // LOADS + 1 loads of each wave; after the last block they repeat it, into buffers that are not read
     auto load = [&](int buffer, int i) {
         char* to = lds + buffer * STAGE;
@@ -118,11 +146,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
     };
 
     f32x4 acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
     struct Codes {
         u32x4 x, y;
     };
@@ -157,139 +180,187 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
     static_assert(FM % 2 == 0, "fragments in pairs");
     Codes a[2], b[FN];
     float sa[2];
-    auto halves = [](const Codes& c, auto fmt, u32x4 h[4]) {
+    auto halves = [](const Codes& c, auto fmt, float f, u32x4 h[4]) {
         constexpr int F = decltype(fmt)::value;
-        h[0] = f8_half8<F>(c.x.x, c.x.y); h[1] = f8_half8<F>(c.x.z, c.x.w);
-        h[2] = f8_half8<F>(c.y.x, c.y.y); h[3] = f8_half8<F>(c.y.z, c.y.w);
+        h[0] = f8_half8<F>(c.x.x, c.x.y, f); h[1] = f8_half8<F>(c.x.z, c.x.w, f);
+        h[2] = f8_half8<F>(c.y.x, c.y.y, f); h[3] = f8_half8<F>(c.y.z, c.y.w, f);
     };
     constexpr std::integral_constant<int, AF> af;
     constexpr std::integral_constant<int, BF> bf;
-    if (steps > 0) {
+    // all products, with scales as they are or taken apart
+    auto run = [&](auto apart) __attribute__((always_inline)) {
+        constexpr bool APART = decltype(apart)::value;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int i = 0; i <= LOADS; ++i) load(s, i);
-            advance(s);
-            asm volatile("" ::: "memory");              // in this order: the waits count on it
-        }
-        f8_barrier<(NS - 1) * (LOADS + 1)>();
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        begin();
+        if (steps > 0) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) b[j] = read_b(lds, j);
+            for (int s = 0; s < NS; ++s) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            a[i] = read_a(lds, i);
-            sa[i] = read_sa(lds, i);
-        }
-        read_sb(lds);
-    }
-    int buffer = 0;
-    for (int t = 0; t < steps; ++t) {
-        const char* cur = lds + buffer * STAGE;
-        const int after = buffer + 1 == NS ? 0 : buffer + 1;
-        const char* next = lds + after * STAGE;
-        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        f32x4 p[2][FN];
-        float scale[2];
-        // the next block has to be there, and every wave to have read this one
-        auto turn = [&] {
-            f8_barrier<(NS - 2) * (LOADS + 1)>();
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        // B first: a lane then holds four consecutive columns of one output row
-        if constexpr (!EXACT) {
-#pragma unroll
-            for (int i = 0; i < FM - 2; ++i) {
-                scale[i & 1] = BTILES ? sa[i & 1] * sb[0].x : sa[i & 1];
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    p[i & 1][j] = mfma_f8<BF, AF>(eight(b[j]), eight(a[i & 1]), zero);
-                    if (i > 0) add(i - 1, j, p[(i - 1) & 1][j], scale[(i - 1) & 1]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                a[i & 1] = read_a(cur, i + 2);
-                sa[i & 1] = read_sa(cur, i + 2);
-                asm volatile("" ::: "memory");          // the reads stay ahead of the next products
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i <= LOADS; ++i) load(s, i);
+                advance(s);
+                asm volatile("" ::: "memory");              // in this order: the waits count on it
             }
-            turn();
-            float left[2];
+            f8_barrier<(NS - 1) * (LOADS + 1)>();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) left[k] = BTILES ? sa[k] * sb[0].x : sa[k];
-            f32x4 r[2][2];
+            for (int j = 0; j < FN; ++j) b[j] = read_b(lds, j);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a[i] = read_a(lds, i);
+                sa[i] = read_sa(lds, i);
+            }
+            read_sb(lds);
+        }
+        int buffer = 0;
+        for (int t = 0; t < steps; ++t) {
+            const char* cur = lds + buffer * STAGE;
+            const int after = buffer + 1 == NS ? 0 : buffer + 1;
+            const char* next = lds + after * STAGE;
+            const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+            F8Factor<EXACT> fa[2] = {1, 1}, fb[FN];
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    r[j & 1][k] = mfma_f8<BF, AF>(eight(b[j]), eight(a[k]), zero);
-                    if (j > 0) add(FM - 2 + k, j - 1, r[1 - (j & 1)][k], left[k]);
-                    else if constexpr (FM > 2)
-#pragma unroll
-                        for (int l = k * FN / 2; l < (k + 1) * FN / 2; ++l) add(FM - 3, l, p[(FM - 3) & 1][l], scale[(FM - 3) & 1]);
-                    if (k == 1) b[j] = read_b(next, j);
-                    if (j + 1 == FN) {
-                        a[k] = read_a(next, k);
-                        sa[k] = read_sa(next, k);
-                    }
-#pragma unroll
-                    for (int l = (2 * j + k) * (LOADS + 1) / (2 * FN); l < (2 * j + k + 1) * (LOADS + 1) / (2 * FN); ++l) load(buffer, l);
-                    asm volatile("" ::: "memory");
-                    __builtin_amdgcn_sched_barrier(0);
+                fb[j] = 1;
+                if constexpr (APART && !BTILES) {
+                    float unused;
+                    fb[j] = f8_take<EXACT>(*reinterpret_cast<const float*>(cur + ROWS + (BM + wn + 16 * j + li) * 4), unused);
+                    sb[j] = f8_rest<EXACT>(sb[j]);
                 }
             }
+            if constexpr (APART && BTILES) {
+                float rest;
+                fb[0] = f8_take<EXACT>(sb[0].x, rest);
+                sb[0].x = rest;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) add(FM - 2 + k, FN - 1, r[(FN - 1) & 1][k], left[k]);
-        } else {
-            u32x4 bh[FN][4];
+                for (int j = 1; j < FN; ++j) fb[j] = fb[0];
+            }
+            auto take_a = [&](int k) {
+                if constexpr (APART) fa[k] = f8_take<EXACT>(sa[k], sa[k]);
+            };
+            auto product = [&](int j, int k) {
+                if constexpr (APART) return mfma_f8<BF, AF>(eight(b[j]), eight(a[k]), zero, (int)fb[j], (int)fa[k]);
+                else return mfma_f8<BF, AF>(eight(b[j]), eight(a[k]), zero);
+            };
+            f32x4 p[2][FN];
+            float scale[2];
+            // the next block has to be there, and every wave to have read this one
+            auto turn = [&] {
+                f8_barrier<(NS - 2) * (LOADS + 1)>();
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            // B first: a lane then holds four consecutive columns of one output row
+            if constexpr (!EXACT) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) halves(b[j], bf, bh[j]);
+                for (int i = 0; i < FM - 2; ++i) {
+                    take_a(i & 1);
+                    scale[i & 1] = BTILES ? sa[i & 1] * sb[0].x : sa[i & 1];
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                scale[i & 1] = BTILES ? sa[i & 1] * sb[0].x : sa[i & 1];
-                u32x4 ah[4];
-                halves(a[i & 1], af, ah);
-                if (i + 2 < FM) {
+                    for (int j = 0; j < FN; ++j) {
+                        p[i & 1][j] = product(j, i & 1);
+                        if (i > 0) add(i - 1, j, p[(i - 1) & 1][j], scale[(i - 1) & 1]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                     a[i & 1] = read_a(cur, i + 2);
                     sa[i & 1] = read_sa(cur, i + 2);
-                }
-                if (i + 1 == FM) {
-                    turn();
-#pragma unroll
-                    for (int l = 0; l <= LOADS; ++l) load(buffer, l);
-                }
-                asm volatile("" ::: "memory");          // the reads stay ahead of the products
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) p[i & 1][j] = mfma16<kBF16>(bh[j][h], ah[h], h ? p[i & 1][j] : zero);
-#pragma unroll
-                    for (int j = h * FN / 4; j < (h + 1) * FN / 4; ++j)
-                        if (i > 0) add(i - 1, j, p[(i - 1) & 1][j], scale[(i - 1) & 1]);
+                    asm volatile("" ::: "memory");          // the reads stay ahead of the next products
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                turn();
+                float left[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    take_a(k);
+                    left[k] = BTILES ? sa[k] * sb[0].x : sa[k];
+                }
+                f32x4 r[2][2];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        r[j & 1][k] = product(j, k);
+                        if (j > 0) add(FM - 2 + k, j - 1, r[1 - (j & 1)][k], left[k]);
+                        else if constexpr (FM > 2)
+#pragma unroll
+                            for (int l = k * FN / 2; l < (k + 1) * FN / 2; ++l) add(FM - 3, l, p[(FM - 3) & 1][l], scale[(FM - 3) & 1]);
+                        if (k == 1) b[j] = read_b(next, j);
+                        if (j + 1 == FN) {
+                            a[k] = read_a(next, k);
+                            sa[k] = read_sa(next, k);
+                        }
+#pragma unroll
+                        for (int l = (2 * j + k) * (LOADS + 1) / (2 * FN); l < (2 * j + k + 1) * (LOADS + 1) / (2 * FN); ++l) load(buffer, l);
+                        asm volatile("" ::: "memory");
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) add(FM - 2 + k, FN - 1, r[(FN - 1) & 1][k], left[k]);
+            } else {
+                u32x4 bh[FN][4];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) halves(b[j], bf, (float)fb[j], bh[j]);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    take_a(i & 1);
+                    scale[i & 1] = BTILES ? sa[i & 1] * sb[0].x : sa[i & 1];
+                    u32x4 ah[4];
+                    halves(a[i & 1], af, (float)fa[i & 1], ah);
+                    if (i + 2 < FM) {
+                        a[i & 1] = read_a(cur, i + 2);
+                        sa[i & 1] = read_sa(cur, i + 2);
+                    }
+                    if (i + 1 == FM) {
+                        turn();
+#pragma unroll
+                        for (int l = 0; l <= LOADS; ++l) load(buffer, l);
+                    }
+                    asm volatile("" ::: "memory");          // the reads stay ahead of the products
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) p[i & 1][j] = mfma16<kBF16>(bh[j][h], ah[h], h ? p[i & 1][j] : zero);
+#pragma unroll
+                        for (int j = h * FN / 4; j < (h + 1) * FN / 4; ++j)
+                            if (i > 0) add(i - 1, j, p[(i - 1) & 1][j], scale[(i - 1) & 1]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j) b[j] = read_b(next, j);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    a[k] = read_a(next, k);
+                    sa[k] = read_sa(next, k);
+                }
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < FN; ++j) add(FM - 1, j, p[(FM - 1) & 1][j], scale[(FM - 1) & 1]);
             }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) b[j] = read_b(next, j);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                a[k] = read_a(next, k);
-                sa[k] = read_sa(next, k);
-            }
-            asm volatile("" ::: "memory");
-#pragma unroll
-            for (int j = 0; j < FN; ++j) add(FM - 1, j, p[(FM - 1) & 1][j], scale[(FM - 1) & 1]);
+            read_sb(next);
+            advance(t + NS);
+            buffer = after;
         }
-        read_sb(next);
-        advance(t + NS);
-        buffer = after;
-    }
-    f8_barrier<0>();                    // no load to LDS outlives its workgroup
+        f8_barrier<0>();                // no load to LDS is under way, and every wave has read its last block
+    };
+    run(std::false_type{});
+    f8_store(g.accumulate, steps > 0,
+             [&] __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int m = m0 + wm + 16 * i + li;
+                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; j += 2) mx_store_pair(g, m, n0 + wn + 16 * j, q, acc[i][j], acc[i][j + 1]);
-    }
+                     for (int j = 0; j < FN; j += 2)
+                         mx_store_pair(g, m0 + wm + 16 * i + li, n0 + wn + 16 * j, q, acc[i][j], acc[i][j + 1]);
+             },
+             [&] __attribute__((always_inline)) {
+                 return f8_again<BM, NT / 64>(g, acc, m0, wm, n0 + wn, f8_least<AF, BF>(steps), reinterpret_cast<uint64_t*>(lds));
+             },
+             [&] __attribute__((always_inline)) {
+                 __syncthreads();
+                 run(std::true_type{});
+             });
 }
 
 // ------------------------------------------------------- few tiles, a long contraction
@@ -306,7 +377,8 @@ __global__ __launch_bounds__(KS * (BM / WM) * (BN / WN) * 64) void k_f8_split(F8
     constexpr int STAGE = KS * BLOCK + NT * 4;
     static_assert(BM % PASS_ROWS == 0 && BN % PASS_ROWS == 0 && PASS_ROWS % 8 == 0, "whole passes per operand");
     static_assert(KS * SR <= NT && kF8Block % WN == 0, "a scale for each thread at most; a wave's columns in one tile");
-    static_assert(KS * WAVES * FM * FN * 1024 <= NS * STAGE, "the sums fit where the codes were");
+    constexpr int SUMS = KS * WAVES * FM * FN * 1024;
+    static_assert(SUMS + F8Words<BM, NT / 64>::count * 8 <= NS * STAGE, "the sums fit where the codes were");
     __shared__ __attribute__((aligned(16))) char lds[NS * STAGE];
 
     int tm, tn;
@@ -350,98 +422,130 @@ __global__ __launch_bounds__(KS * (BM / WM) * (BN / WN) * 64) void k_f8_split(F8
         load_to_lds<4>(s0 + min(stage * KS + sk, steps - 1) * s_step, s_off, to + KS * BLOCK + wave * 256);
     };
 
+    static_assert(FM * FN / 2 == KS && FM % 2 == 0 && FN == 2, "a pair of a wave's fragments for each group");
     f32x4 acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int lo = (q ^ (li & 7)) << 4, hi = ((q + 4) ^ (li & 7)) << 4;
 
-    for (int s = 0; s < NS - 1 && steps > 0; ++s) {
-        issue(s);
-        asm volatile("" ::: "memory");                  // in this order: the waits count on it
-    }
-    for (int s = 0; s < stages; ++s) {
-        // the stage is there, and every wave has read the one before, whose buffer is filled anew
-        f8_barrier<(NS - 2) * (LOADS + 1)>();
-        issue(s + NS - 1);
-        if (s * KS + group >= steps) continue;
-        const char* cur = lds + s % NS * STAGE + group * BLOCK;
-        const float* sc = reinterpret_cast<const float*>(lds + s % NS * STAGE + KS * BLOCK) + group * SR;
-        auto read = [&](int row, u32x4& x, u32x4& y) {
-            x = *reinterpret_cast<const u32x4*>(cur + (row + li) * 128 + lo);
-            y = *reinterpret_cast<const u32x4*>(cur + (row + li) * 128 + hi);
-        };
-        u32x4 ax[FM], ay[FM], bx[FN], by[FN];
-        float sa[FM];
-        f32x4 sb[BTILES ? 1 : FN];
+    f32x4 v[1][FN];
+    // all products, with scales as they are or taken apart
+    auto run = [&](auto apart) __attribute__((always_inline)) {
+        constexpr bool APART = decltype(apart)::value;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) read(BM + wn + 16 * j, bx[j], by[j]);
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int i = 0; i < FM; ++i) read(wm + 16 * i, ax[i], ay[i]);
-        if constexpr (BTILES) {
-            sb[0].x = sc[BM + wn / kF8Block];
-        } else {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(sc + BM + wn + 16 * j + 4 * q);
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < NS - 1 && steps > 0; ++s) {
+            issue(s);
+            asm volatile("" ::: "memory");                  // in this order: the waits count on it
         }
+        for (int s = 0; s < stages; ++s) {
+            // the stage is there, and every wave has read the one before, whose buffer is filled anew
+            f8_barrier<(NS - 2) * (LOADS + 1)>();
+            issue(s + NS - 1);
+            if (s * KS + group >= steps) continue;
+            const char* cur = lds + s % NS * STAGE + group * BLOCK;
+            const float* sc = reinterpret_cast<const float*>(lds + s % NS * STAGE + KS * BLOCK) + group * SR;
+            auto read = [&](int row, u32x4& x, u32x4& y) {
+                x = *reinterpret_cast<const u32x4*>(cur + (row + li) * 128 + lo);
+                y = *reinterpret_cast<const u32x4*>(cur + (row + li) * 128 + hi);
+            };
+            u32x4 ax[FM], ay[FM], bx[FN], by[FN];
+            float sa[FM];
+            f32x4 sb[BTILES ? 1 : FN];
 #pragma unroll
-        for (int i = 0; i < FM; ++i) sa[i] = sc[wm + 16 * i + li] * (BTILES ? sb[0].x : 1.0f);
-        u32x4 bh[EXACT ? FN : 1][4];
-        if constexpr (EXACT) {
+            for (int j = 0; j < FN; ++j) read(BM + wn + 16 * j, bx[j], by[j]);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) read(wm + 16 * i, ax[i], ay[i]);
+            if constexpr (BTILES) {
+                sb[0].x = sc[BM + wn / kF8Block];
+            } else {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(sc + BM + wn + 16 * j + 4 * q);
+            }
+            F8Factor<EXACT> fa[FM] = {}, fb[FN] = {};
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                bh[j][0] = f8_half8<BF>(bx[j].x, bx[j].y); bh[j][1] = f8_half8<BF>(bx[j].z, bx[j].w);
-                bh[j][2] = f8_half8<BF>(by[j].x, by[j].y); bh[j][3] = f8_half8<BF>(by[j].z, by[j].w);
+                fb[j] = 1;
+                if constexpr (APART) {
+                    float rest;
+                    fb[j] = f8_take<EXACT>(BTILES ? sb[0].x : sc[BM + wn + 16 * j + li], rest);
+                    if constexpr (!BTILES) sb[j] = f8_rest<EXACT>(sb[j]);
+                }
             }
-        }
+            if constexpr (APART && BTILES) sb[0] = f8_rest<EXACT>(sb[0]);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            f32x4 p[FN];
+            for (int i = 0; i < FM; ++i) {
+                sa[i] = sc[wm + 16 * i + li];
+                fa[i] = 1;
+                if constexpr (APART) fa[i] = f8_take<EXACT>(sa[i], sa[i]);
+                if constexpr (BTILES) sa[i] *= sb[0].x;
+            }
+            u32x4 bh[EXACT ? FN : 1][4];
             if constexpr (EXACT) {
-                const u32x4 ah[4] = {f8_half8<AF>(ax[i].x, ax[i].y), f8_half8<AF>(ax[i].z, ax[i].w),
-                                     f8_half8<AF>(ay[i].x, ay[i].y), f8_half8<AF>(ay[i].z, ay[i].w)};
-#pragma unroll
-                for (int j = 0; j < FN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) p[j] = mfma16<kBF16>(bh[j][h], ah[h], p[j]);
-            } else {
-                const i32x8 a = {(int)ax[i].x, (int)ax[i].y, (int)ax[i].z, (int)ax[i].w,
-                                 (int)ay[i].x, (int)ay[i].y, (int)ay[i].z, (int)ay[i].w};
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
-                    const i32x8 b = {(int)bx[j].x, (int)bx[j].y, (int)bx[j].z, (int)bx[j].w,
-                                     (int)by[j].x, (int)by[j].y, (int)by[j].z, (int)by[j].w};
-                    p[j] = mfma_f8<BF, AF>(b, a, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                    const float f = (float)fb[j];
+                    bh[j][0] = f8_half8<BF>(bx[j].x, bx[j].y, f); bh[j][1] = f8_half8<BF>(bx[j].z, bx[j].w, f);
+                    bh[j][2] = f8_half8<BF>(by[j].x, by[j].y, f); bh[j][3] = f8_half8<BF>(by[j].z, by[j].w, f);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int i = 0; i < FM; ++i) {
+                f32x4 p[FN];
+                if constexpr (EXACT) {
+                    const float f = (float)fa[i];
+                    const u32x4 ah[4] = {f8_half8<AF>(ax[i].x, ax[i].y, f), f8_half8<AF>(ax[i].z, ax[i].w, f),
+                                         f8_half8<AF>(ay[i].x, ay[i].y, f), f8_half8<AF>(ay[i].z, ay[i].w, f)};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[j][r], BTILES ? sa[i] : sa[i] * sb[j][r], acc[i][j][r]);
+                    for (int j = 0; j < FN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) p[j] = mfma16<kBF16>(bh[j][h], ah[h], p[j]);
+                } else {
+                    const i32x8 a = {(int)ax[i].x, (int)ax[i].y, (int)ax[i].z, (int)ax[i].w,
+                                     (int)ay[i].x, (int)ay[i].y, (int)ay[i].z, (int)ay[i].w};
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        const i32x8 b = {(int)bx[j].x, (int)bx[j].y, (int)bx[j].z, (int)bx[j].w,
+                                         (int)by[j].x, (int)by[j].y, (int)by[j].z, (int)by[j].w};
+                        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if constexpr (APART) p[j] = mfma_f8<BF, AF>(b, a, zero, (int)fb[j], (int)fa[i]);
+                        else p[j] = mfma_f8<BF, AF>(b, a, zero);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[j][r], BTILES ? sa[i] : sa[i] * sb[j][r], acc[i][j][r]);
+            }
         }
-    }
-    f8_barrier<0>();                    // no load to LDS is under way, and every wave has read its last block
-    f32x4* sums = reinterpret_cast<f32x4*>(lds);
+        f8_barrier<0>();                // no load to LDS is under way, and every wave has read its last block
+        f32x4* sums = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) sums[((group * WAVES + part) * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
-    __syncthreads();
-    // pair p of a wave's fragments is added up by group p % KS
+            for (int j = 0; j < FN; ++j) sums[((group * WAVES + part) * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        // fragments (i, 0) and (i, 1) of a wave are added up by group i
 #pragma unroll
-    for (int p = 0; p < FM * FN / 2; ++p) {
-        if (p % KS != group) continue;
-        f32x4 v[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        for (int h = 0; h < FN; ++h) {
+            v[0][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) v[h] += sums[((k * WAVES + part) * FM * FN + 2 * p + h) * 64 + lane];
-        const int i = 2 * p / FN, j = 2 * p % FN;
-        mx_store_pair(g, m0 + wm + 16 * i + li, n0 + wn + 16 * j, q, v[0], v[1]);
-    }
+            for (int k = 0; k < KS; ++k) v[0][h] += sums[((k * WAVES + part) * FM * FN + group * FN + h) * 64 + lane];
+        }
+    };
+    run(std::false_type{});
+    f8_store(g.accumulate, true,
+             [&] __attribute__((always_inline)) { mx_store_pair(g, m0 + wm + 16 * group + li, n0 + wn, q, v[0][0], v[0][1]); },
+             [&] __attribute__((always_inline)) {
+                 return f8_again<BM, NT / 64>(g, v, m0, wm + 16 * group, n0 + wn, f8_least<AF, BF>(steps),
+                                              reinterpret_cast<uint64_t*>(lds + SUMS));
+             },
+             [&] __attribute__((always_inline)) {
+                 __syncthreads();
+                 run(std::true_type{});
+             });
 }
 
 // ------------------------------------------------------------------------ tile choice

@@ -646,7 +646,9 @@ BITOPT_API int bitopt_f8_dequantize(const uint8_t* codes, const float* scales, i
 /*
  * Product of two F8 matrices: out[m][n] = sum_k a[m][k] b[n][k], a m x k by rows, b n x k by
  * rows or tiles; accumulate != 0 adds it to out.  Each block of 128 is summed by itself,
- * multiplied by its scales and added in fp32; the result is rounded once into out_dtype.  The
+ * multiplied by its scales and added in fp32; the result is rounded once into out_dtype.  Only
+ * elements' products, scales included, and their sums have to lie in fp32's range, not the product
+ * of two scales; a sum beyond it is infinite, or NaN where infinities of both signs meet.  The
  * three products of a linear layer y = x W^T: x (rows) with W (tiles); dy (rows) with W^T
  * (tiles); dy^T (rows) with x^T (rows).
  * With a 16-bit result and more than 32 rows of a, a block's sum runs on the 8-bit matrix
