@@ -111,7 +111,8 @@ int bitopt_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t a_fo
     g.out = out; g.ldo = ldo; g.out_dtype = out_dtype; g.accumulate = accumulate != 0;
     g.M = (int32_t)m; g.N = (int32_t)n; g.K = (int32_t)k;
     if (m <= kF8FewRows) return api_status(launch_f8_few(g, a_format, b_format, b_blocks, as_stream(stream)), fn);
-    if (out_dtype == BITOPT_F32) return api_status(launch_f8_exact(g, a_format, b_format, b_blocks, as_stream(stream)), fn);
+    // what the 8-bit instruction drops shows in fp16 (f8_gemm.h)
+    if (out_dtype != BITOPT_BF16) return api_status(launch_f8_exact(g, a_format, b_format, b_blocks, as_stream(stream)), fn);
     return api_status(launch_f8_fast(g, a_format, b_format, b_blocks, as_stream(stream)), fn);
 }
 

@@ -1,4 +1,4 @@
-// Tiled F8 products with fp32 results, on the 16-bit matrix instructions.
+// Tiled F8 products with fp32 and fp16 results, on the 16-bit matrix instructions.
 #include "f8_gemm.h"
 
 namespace bitopt {

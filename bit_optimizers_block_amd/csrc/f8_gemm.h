@@ -3,10 +3,14 @@
 // Each block of 128 contraction elements is a product of its own, multiplied by its rows' and
 // columns' scales and added to the fp32 sums.  Two ways to that product:
 //   fast   the 8-bit matrix instruction, one for 128 elements.  It aligns the products of a
-//          step to the largest one and drops what lies some 17 bits below: far below half a
-//          step of a 16-bit result, and visible in an fp32 one.
+//          step to the largest one and drops what lies some 17 bits below.
 //   exact  the codes decoded to bf16 in registers (every element is exact there) and four
-//          16-bit matrix instructions, which keep fp32: for fp32 results, at half the rate.
+//          16-bit matrix instructions, which keep fp32: at half the rate.
+// Error of the sums, in norm, as a share of the results' norm (1024 x 1024 x K, K from 128 to 8192, normal
+// values): fast 1.4e-5 (E4M3) and 1.1e-5 (E5M2 x E4M3) at any K, without a bias, at most 2e-5 of the sum
+// of magnitudes at K = 128 and 1.2e-6 at 8192; exact 5e-8 to 1e-7.  Rounding to bf16 is 1.657e-3 with either: one
+// result in a hundred rounds to the other side.  Rounding to fp16 is 2.074e-4 and became 2.079e-4, six in a hundred.
+// So bf16 results are fast, fp16 and fp32 ones exact.
 #pragma once
 
 #include <algorithm>

@@ -651,10 +651,11 @@ BITOPT_API int bitopt_f8_dequantize(const uint8_t* codes, const float* scales, i
  * of two scales; a sum beyond it is infinite, or NaN where infinities of both signs meet.  The
  * three products of a linear layer y = x W^T: x (rows) with W (tiles); dy (rows) with W^T
  * (tiles); dy^T (rows) with x^T (rows).
- * With a 16-bit result and more than 32 rows of a, a block's sum runs on the 8-bit matrix
+ * With a bf16 result and more than 32 rows of a, a block's sum runs on the 8-bit matrix
  * instruction, which aligns the products to the largest one and drops what lies some 17 bits
- * below it; with an fp32 result, and for up to 32 rows, on decoded elements, where products
- * are exact and sums are those of fp32.
+ * below it (in norm 1.4e-5 of the results, whose rounding to bf16 is 1.7e-3); with an fp16 or
+ * fp32 result, at half the rate, and for up to 32 rows, on decoded elements, where products are
+ * exact and sums are those of fp32.
  * Up to 32 rows of a take a form that reads b once.  k above 2^24 gives UNSUPPORTED, and so
  * do products that one launch does not hold: some 2^38 results, or 2^27 columns for up to
  * 32 rows.

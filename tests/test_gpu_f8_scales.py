@@ -26,7 +26,7 @@ def _gpu():
 
 
 def fast(m, out):
-    return m > 32 and out != "f32"
+    return m > 32 and out == "bf16"
 
 
 def check(y, va, vb, out, m, old=None, what=""):
