@@ -449,9 +449,9 @@ static bool small_sort(int64_t count, int64_t vocab) {
 EmbeddingSpace embedding_space(int64_t count, int64_t vocab, int64_t width) {
     EmbeddingSpace s{};
     // Eight places are one round of loads; more of them in a window, fewer parts to join.  us, added
-    // gradient, with up to 2048, 1024, 768 and 512 windows: 8192 tokens, width 2048: 49.5, 49.4, 45.9,
-    // 46.5 (all the same token: 119, 118, 73, 73); 16384, 2048: 82, 73, 69, 69; 32768, 1024: 86, 79, 81,
-    // 80; 65536, 512: 82, 83, 101, 101, where a workgroup takes four windows.
+    // gradient, with up to 2048, 1024, 768 and 512 windows (768 are 512 where count is a power of two): 8192
+    // tokens, width 2048: 49.5, 49.4, 45.9, 46.5 (all the same token: 119, 118, 73, 73); 16384, 2048: 82, 73, 69,
+    // 69; 32768, 1024: 86, 79, 81, 80; 65536, 512: 82, 83, 101, 101, where a workgroup takes four windows.
     const int64_t most = width > 512 ? 768 : 1024;
     s.span = 8;
     while (most * s.span < count) s.span *= 2;

@@ -714,7 +714,8 @@ BITOPT_API int bitopt_mx_embedding_forward(const void* tokens, int32_t token_typ
  * without a token are zero.  accumulate != 0 adds the sums to dtable (a tied head's gradient,
  * earlier micro-batches) and touches only rows that have a token.  Padding takes no
  * part.  Tokens are sorted by number, each sum is taken in fp32 in the order of the batch (in
- * parts where the sorted order is cut, at places that follow from count), rounded once.
+ * parts where the sorted order is cut, at places that follow from count and width, so columns
+ * by themselves may get other last bits than within a wider table), rounded once.
  *   workspace   device, 16-byte aligned, at least bitopt_embedding_workspace_bytes(count,
  *               vocab, width) bytes (-1: a size < 0 or above 2^30; no fewer for a larger
  *               count), not needed between calls; calls that may run at the same time need
