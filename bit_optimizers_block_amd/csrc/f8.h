@@ -16,7 +16,7 @@
 namespace bitopt {
 
 constexpr int kF8E4M3 = 0, kF8E5M2 = 1;       // the matrix instruction's own numbers of the formats
-constexpr int kF8Rows = 0, kF8Tiles = 1;
+constexpr int kF8Tiles = 1;                    // else rows
 constexpr int kF8Block = 128;
 
 __host__ __device__ constexpr int64_t f8_blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }

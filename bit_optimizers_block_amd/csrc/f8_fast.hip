@@ -1,4 +1,4 @@
-// Tiled F8 products with 16-bit results, on the 8-bit matrix instructions.
+// Tiled F8 products with bf16 results, on the 8-bit matrix instructions.
 #include "f8_gemm.h"
 
 namespace bitopt {

@@ -36,7 +36,7 @@ template <int DT, int OUT> __global__ __launch_bounds__(kThreads) void k_embeddi
         const int n = (int)min((int64_t)PER, a.width - e);
         const int64_t id = token_at(a.tokens, a.wide, row);
         float v[PER] = {};
-        if ((uint64_t)id < (uint64_t)a.vocab) ld_row<DT, PER, false>(a.table, id * a.ldt + e, n, e, v);
+        if ((uint64_t)id < (uint64_t)a.vocab) ld_row<DT, PER>(a.table, id * a.ldt + e, n, e, v);
 #pragma unroll
         for (int j = 0; j < PER; ++j) v[j] *= a.scale;
         st_row<OUT, PER>(a.out, row * a.ldo + e, n, v);
@@ -286,7 +286,7 @@ __device__ __forceinline__ void put_row(const EmbeddingGradArgs& a, uint32_t key
     const int n = (int)min((int64_t)8, a.width - 8 * (int64_t)item);
     float v[8];
     if (a.accumulate) {
-        ld_row<OUT, 8, false>(a.out, e, n, 8 * (int64_t)item, v);
+        ld_row<OUT, 8>(a.out, e, n, 8 * (int64_t)item, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += sum[j] * a.scale;
     } else {

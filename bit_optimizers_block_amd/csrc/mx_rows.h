@@ -78,16 +78,16 @@ template <int DT, bool NT = true> __device__ __forceinline__ void st_item(void* 
     }
 }
 
-// PER elements of a row whatever the type: eight (fp32 in two loads or stores), or four (16-bit
-// ones in half a load).  A matrix of fp32 is best written in fours: lanes that write eight leave
+// PER elements of a row whatever the type: eight (fp32 in two loads or stores), or four (fp32, and
+// 16-bit loads of half the width).  A matrix of fp32 is best written in fours: lanes that write eight leave
 // every other 16 bytes to the next store, and such streamed stores reach 2 TB/s instead of 6.
-template <int DT, int PER, bool NT>
+template <int DT, int PER>
 __device__ __forceinline__ void ld_row(const void* base, int64_t e, int n, int64_t before, float v[PER]) {
     if constexpr (PER == kPer<DT>) {
-        ld_item<DT, NT>(base, e, n, before, v);
+        ld_item<DT, false>(base, e, n, before, v);
     } else if constexpr (DT == kF32) {
-        ld_item<DT, NT>(base, e, n, before, v);
-        ld_item<DT, NT>(base, e + 4, n - 4, before + 4, v + 4);
+        ld_item<DT, false>(base, e, n, before, v);
+        ld_item<DT, false>(base, e + 4, n - 4, before + 4, v + 4);
     } else {
         const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + e;
         if (n >= 4) {
@@ -101,22 +101,9 @@ __device__ __forceinline__ void ld_row(const void* base, int64_t e, int n, int64
     }
 }
 template <int DT, int PER, bool NT = true> __device__ __forceinline__ void st_row(void* base, int64_t e, int n, const float v[PER]) {
-    if constexpr (PER == kPer<DT>) {
-        st_item<DT, NT>(base, e, n, v);
-    } else if constexpr (DT == kF32) {
-        st_item<DT, NT>(base, e, n, v);
-        st_item<DT, NT>(base, e + 4, n - 4, v + 4);
-    } else {
-        uint16_t* p = reinterpret_cast<uint16_t*>(base) + e;
-        const uint32_t r[2] = {narrow2<DT>(v[0], v[1]), narrow2<DT>(v[2], v[3])};
-        if (n >= 4) {
-            st8_a2(p, u32x2{r[0], r[1]});
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < n) gbl(p)[j] = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
-        }
-    }
+    static_assert(DT == kF32 || PER == kPer<DT>, "16-bit elements are written in eights");
+    st_item<DT, NT>(base, e, n, v);
+    if constexpr (PER > kPer<DT>) st_item<DT, NT>(base, e + 4, n - 4, v + 4);
 }
 
 // Eight elements of a row of at least eight as they lie, from column c or, near its end, the row's
