@@ -115,27 +115,34 @@ template <int FMT> __device__ __forceinline__ void f8_decode4(uint32_t c, float 
 // zero.  Where one is left, its tile is taken once more with every scale as f s: f, a power of two, goes into p
 // by way of the elements or of the matrix instruction, and the product of two s stays in range.  Results
 // that were right keep their bits in that.
-// Measured, bf16 results: 8192 x 8192 x 2048 131.5 -> 134.1 us, 8192 x 2048 x 8192 112.1 -> 112.2; with 2% of A's rows
-// zero 131.6 -> 141.2, 110.3 -> 112.2.  Inside the loops it costs more: every scale taken apart 114 -> 119 (B by rows
-// 130 -> 147, fp32 results 250 -> 274), a branch to that where a block needs it spills.
+// Measured, bf16 results, without and with it: 8192 x 8192 x 2048 127.1 and 128.1 us, 8192 x 2048 x 8192 108.6 and 108.2,
+// 512 x 2048 x 2048 7.2 and 7.1; with 2% of A's rows zero 128.6 and 134.5, 108.3 and 110.5, 7.2 and 7.9; all zero 107 and 145.
+// Inside the loops it costs more: every scale taken apart 114 and 119 (B by rows 130 and 147, fp32 results 250 and 274), a
+// branch to that where a block needs it spills.
 template <int AF, int BF> __device__ __forceinline__ float f8_least(int blocks) {
     return (float)blocks * (float)(kF8Block * 0x1p-126 * kF8Top<AF> * kF8Top<BF>);
 }
 __device__ __forceinline__ bool f8_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
 
-// Of the rows of codes whose bits are set, those that hold a code which is neither 0 nor -0; by a whole wave.
+// Of the rows of codes whose bits are set, those that hold a code which is neither 0 nor -0; by a whole wave,
+// two rows at a time.
 __device__ __forceinline__ uint64_t f8_hold(const uint8_t* codes, int64_t bytes, uint64_t rows) {
     uint64_t held = 0;
-    for (; rows; rows &= rows - 1) {
-        const uint8_t* row = codes + __builtin_ctzll(rows) * bytes;
-        uint32_t any = 0;
+    while (rows) {
+        const uint64_t one = rows & -rows, rest = rows ^ one, two = rest ? rest & -rest : one;
+        const uint8_t *p = codes + __builtin_ctzll(one) * bytes, *q = codes + __builtin_ctzll(two) * bytes;
+        uint32_t x = 0, y = 0;
         for (int64_t c = 16 * (threadIdx.x & 63); c < bytes; c += 4096)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const u32x4 w = *gbl(reinterpret_cast<const u32x4*>(row + min(c + 1024 * k, bytes - 16)));
-                any |= w.x | w.y | w.z | w.w;
+                const int64_t at = min(c + 1024 * k, bytes - 16);
+                const u32x4 v = *gbl(reinterpret_cast<const u32x4*>(p + at)), w = *gbl(reinterpret_cast<const u32x4*>(q + at));
+                x |= v.x | v.y | v.z | v.w;
+                y |= w.x | w.y | w.z | w.w;
             }
-        if (f8_any((any & 0x7f7f7f7fu) != 0)) held |= rows & -rows;
+        if (f8_any((x & 0x7f7f7f7fu) != 0)) held |= one;
+        if (f8_any((y & 0x7f7f7f7fu) != 0)) held |= two;
+        rows &= ~(one | two);
     }
     return held;
 }
@@ -184,68 +191,73 @@ __device__ __forceinline__ bool f8_columns(const F8GemmArgs& g, const f32x4 (&v)
     return f8_hold(g.b + (int64_t)n * g.row_bytes, g.row_bytes, cols) != 0;
 }
 
-// Whether a workgroup's results have to be taken once more, those of this wave v, from row m0 + wm and column n.
-// words: F8Words<BM, WAVES>::count of LDS.
+// Whether a workgroup's results have to be taken once more, those of this wave v, from row m0 + wm and column n; it
+// is the `part`-th of PARTS waves with the same rows.  words: F8Words<BM, WAVES> of LDS.
 template <int BM, int WAVES> struct F8Words {
-    static constexpr int rows = (BM + 63) / 64, each = rows + 1, count = 2 * WAVES * each + WAVES;
-    static_assert(WAVES * each <= 64, "a word for each lane");
+    static constexpr int rows = (BM + 63) / 64, count = WAVES * (2 * rows + 1);
+    static_assert(WAVES * rows <= 64, "a word for each lane");
 };
-template <int BM, int WAVES, int R, int C>
-__device__ __forceinline__ bool f8_again(const F8GemmArgs& g, const f32x4 (&v)[R][C], int m0, int wm, int n, float least,
+template <int BM, int WAVES, int PARTS, int R, int C>
+__device__ __forceinline__ bool f8_again(const F8GemmArgs& g, const f32x4 (&v)[R][C], int m0, int wm, int part, int n, float least,
                                          uint64_t* words) {
-    constexpr int W = F8Words<BM, WAVES>::rows, E = F8Words<BM, WAVES>::each;
+    constexpr int W = F8Words<BM, WAVES>::rows;
+    constexpr uint64_t kEach = PARTS == 1 ? ~0ull : PARTS == 2 ? 0x5555555555555555ull : 0x1111111111111111ull;
+    static_assert(PARTS == 1 || PARTS == 2 || PARTS == 4, "every PARTS-th row");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15;
+    uint64_t *low_rows = words + WAVES, *zero_rows = low_rows + WAVES * W;
     float low[R];
     const bool bad = f8_lows(v, low);
-    uint64_t mine[W] = {};
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const uint64_t rows = f8_rows_with(low[i] < least && m0 + wm + 16 * i + li < g.M);
+    for (int i = 0; i < R; ++i) any |= low[i] < least;
+    const bool small = f8_any(any);
+    uint64_t mine[W] = {};                              // rows with a result below `least`
+    if (__builtin_expect(small, 0)) {
 #pragma unroll
-        for (int w = 0; w < W; ++w)
-            if ((wm + 16 * i) / 64 == w) mine[w] |= rows << (wm + 16 * i) % 64;
+        for (int i = 0; i < R; ++i) {
+            const uint64_t rows = f8_rows_with(low[i] < least && m0 + wm + 16 * i + li < g.M);
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if ((wm + 16 * i) / 64 == w) mine[w] |= rows << (wm + 16 * i) % 64;
+        }
+        // a row of zeros is one in each of the waves with these rows, which share them out
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const uint64_t own = mine[w] & kEach << part;
+            const uint64_t zero = own & ~f8_hold(g.a + (int64_t)(m0 + 64 * w) * g.row_bytes, g.row_bytes, own);
+            if (lane == 0) {
+                low_rows[wave * W + w] = mine[w];
+                zero_rows[wave * W + w] = zero;
+            }
+        }
     }
-    if (lane == 0) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) words[wave * E + w] = mine[w];
-        words[wave * E + W] = bad;
-    }
+    if (lane == 0) words[wave] = (bad ? 2 : 0) | (small ? 1 : 0);
     __syncthreads();
-    const uint64_t word = lane < WAVES * E ? words[lane] : 0;
-    const bool set = word != 0;
-    if (__builtin_expect(!f8_any(set), 1)) return false;
-    if (f8_any(set && lane % E == W)) return true;
-    // rows that hold a code, each looked at by one wave
-    uint64_t* held = words + WAVES * E;
-    int turn = 0;
+    const uint64_t flags = lane < WAVES ? words[lane] : 0;
+    if (__builtin_expect(!f8_any(flags != 0), 1)) return false;
+    if (f8_any(flags & 2)) return true;
+    // lane W k + w: rows 64 w .. of wave k that are left
+    const bool in = lane < WAVES * W && words[lane / W];
+    uint64_t zero = in ? zero_rows[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        uint64_t rows = 0;
-#pragma unroll
-        for (int k = 0; k < WAVES; ++k)
-            rows |= (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)word, k * E + w) |
-                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(word >> 32), k * E + w) << 32;
-        uint64_t own = 0;
-        for (; rows; rows &= rows - 1)
-            if (turn++ % WAVES == wave) own |= rows & -rows;
-        const uint64_t found = f8_hold(g.a + (int64_t)(m0 + 64 * w) * g.row_bytes, g.row_bytes, own);
-        if (lane == 0) held[wave * W + w] = found;
-    }
-    __syncthreads();
-    if (!f8_any(lane < WAVES * W && held[lane] != 0)) return false;
-    // in those rows, columns that hold one
+    for (int k = W; k < WAVES * W; k *= 2) zero |= __shfl_xor(zero, k);
+    if (!f8_any(in && (low_rows[lane] & ~zero))) return false;
+    // and in those, columns that hold a code
     bool row[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        uint64_t found = 0;
-        for (int k = 0; k < WAVES; ++k) found |= held[k * W + (wm + 16 * i) / 64];
-        row[i] = found >> ((wm + 16 * i) % 64 + li) & 1;
+        const int w = (wm + 16 * i) / 64;
+        uint64_t left = 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            if (k == w) left = mine[k] & ~__shfl(zero, k);
+        row[i] = left >> ((wm + 16 * i) % 64 + li) & 1;
     }
-    uint64_t* again = held + WAVES * E;
-    const bool yes = f8_columns(g, v, row, n, least);
-    if (lane == 0) again[wave] = yes;
+    const bool yes = small && f8_columns(g, v, row, n, least);
+    __syncthreads();                                    // the flags have been read
+    if (lane == 0) words[wave] = yes;
     __syncthreads();
-    return f8_any(lane < WAVES && again[lane] != 0);
+    return f8_any(lane < WAVES && words[lane]);
 }
 
 // The same of 16 x 16 results that one wave has.
@@ -260,8 +272,9 @@ __device__ __forceinline__ bool f8_again(const F8GemmArgs& g, const f32x4 (&v)[1
     return found && f8_columns(g, v, row, n, least);
 }
 
-// Results go out before they are looked at, which then runs beside the stores (ahead of them: 136.1 us for the
-// 134.1 above), and once more where they were taken once more.  Results to be added to old ones wait.
+// Results go out before they are looked at, which then runs beside the stores (8192 x 8192 x 2048, an earlier form of
+// it, behind them and ahead of them: 134.1 and 136.1 us), and once more where they were taken once more.  Results to
+// be added to old ones wait.
 template <class Store, class Again, class Redo>
 __device__ __forceinline__ void f8_store(bool accumulate, bool look, Store store, Again again, Redo redo) {
     if (!accumulate) store();

@@ -359,7 +359,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_f8_gemm(F8GemmAr
                          mx_store_pair(g, m0 + wm + 16 * i + li, n0 + wn + 16 * j, q, acc[i][j], acc[i][j + 1]);
              },
              [&] __attribute__((always_inline)) {
-                 return f8_again<BM, NT / 64>(g, acc, m0, wm, n0 + wn, f8_least<AF, BF>(steps), reinterpret_cast<uint64_t*>(lds));
+                 return f8_again<BM, NT / 64, BN / WN>(g, acc, m0, wm, wn / WN, n0 + wn, f8_least<AF, BF>(steps),
+                                                       reinterpret_cast<uint64_t*>(lds));
              },
              [&] __attribute__((always_inline)) {
                  __syncthreads();
@@ -543,8 +544,8 @@ __global__ __launch_bounds__(KS * (BM / WM) * (BN / WN) * 64) void k_f8_split(F8
     f8_store(g.accumulate, true,
              [&] __attribute__((always_inline)) { mx_store_pair(g, m0 + wm + 16 * group + li, n0 + wn, q, v[0][0], v[0][1]); },
              [&] __attribute__((always_inline)) {
-                 return f8_again<BM, NT / 64>(g, v, m0, wm + 16 * group, n0 + wn, f8_least<AF, BF>(steps),
-                                              reinterpret_cast<uint64_t*>(lds + SUMS));
+                 return f8_again<BM, NT / 64, BN / WN>(g, v, m0, wm + 16 * group, wn / WN, n0 + wn, f8_least<AF, BF>(steps),
+                                                       reinterpret_cast<uint64_t*>(lds + SUMS));
              },
              [&] __attribute__((always_inline)) {
                  __syncthreads();
