@@ -3,7 +3,7 @@
 // Bound by reading B once.  A workgroup takes 16 rows of B, and its waves take blocks of 128
 // contraction elements in turn: a wave's load covers 16 whole lines.  Codes are decoded to
 // bf16 (exact) for the 16-bit matrix instructions, which keep pace with memory here, so one
-// form serves 16-bit and fp32 results (one row x 50257 x 2048: 17.9 us, 5.8 TB/s).  The waves'
+// form serves 16-bit and fp32 results (one row x 50257 x 2048, B by tiles: 17.6 us, 5.9 TB/s).  The waves'
 // sums meet in LDS, in the order of the waves.
 #include <type_traits>
 
@@ -119,8 +119,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_f8_few(F8GemmArgs g) {
 
 // ------------------------------------------------------------------------- launches
 
-// us with four and with eight waves, B by tiles: 1 x 50257 x 2048 20.5 to 22.3, 23.2; 1 x 2048 x 8192
-// 8.9, 7.1; 16 x 8192 x 8192 21.3, 19.7.  Beyond 32 rows the tiled forms are faster: 64 x 8192 x 2048
+// us a launch among others with four and with eight waves, B by tiles: 1 x 50257 x 2048 18.1, 18.6; 1 x 2048 x 8192
+// 8.0, 7.0; 16 x 8192 x 8192 18.3, 17.1; 32 x 8192 x 8192 25.3, 25.0; by rows: 19.5, 23.5; 9.5, 7.6; 19.9, 18.6; 26.6,
+// 26.3.  Beyond 32 rows the tiled forms are faster; us with this form and with those: 64 x 8192 x 2048
 // 13.1 and 8.1, 64 x 50257 x 2048 65 and 39 (17 x 4093 x 1999 5.6 and 7.2).
 template <int AF, int BF, bool BTILES> static hipError_t few(const F8GemmArgs& g, hipStream_t s) {
     const dim3 grid((unsigned)(((int64_t)g.N + 15) / 16));

@@ -84,14 +84,16 @@ template <int SIZE> __device__ __forceinline__ void load_to_lds(const void* base
 // the other for the reads of the next block.  Exact: ahead of the last group; B's decoded fragments
 // leave no registers for the next ones.
 //
-// Bound: the SIMD's instructions.  Matrix and vector instructions of its two waves do not overlap:
-// at 8192 x 2048 x 8192, fast, B by tiles (110 to 117 us, 2350 to 2500 TFLOP/s), the matrix pipes are
-// busy 57% of the cycles and other vector instructions, nearly all of them the 128 additions of a
-// block, another 34%; with the additions left out it takes 101.  LDS is busy 25%, without
-// conflicts.  By rows each addition takes a product of two scales besides (125 to 130 us), and in the
-// exact form the decoding (250).  Where the contraction is short the results' stores show:
-// 8192 x 8192 x 2048 takes 150 to 155 us, some 30 of them 134 MB of results that nothing overlaps (one
-// workgroup a CU; a resident grid whose next tile's loads go ahead of the stores spilled).
+// Bound at 8192 x 2048 x 8192, fast, B by tiles: no pipe by itself.  A launch takes 232 to 242 thousand cycles, 108 to
+// 119 us, and 125 to 135 in a long row of them (2040 to 2550 TFLOP/s): the clock falls from 2.06 to 1.80 GHz.  The
+// matrix pipes are busy 131 thousand of them (54 to 57%), and other vector instructions, nearly all of them the 128
+// additions of a block, issue in 82 thousand (34%).  With the sums left to the matrix instruction, without scales, it
+// takes 215 thousand, 101 to 116 us: two thirds of the additions run beside matrix instructions.  What the other
+// cycles wait for those counters do not tell.  LDS is busy 25%, without conflicts.  By rows each addition takes a product
+// of two scales besides (127 to 149 us), and in the exact form the decoding (243 to 273).  Where the
+// contraction is short the results' stores show: 8192 x 8192 x 2048 takes 128 to 158 us, some 30 of them 134 MB of
+// results that nothing overlaps (one workgroup a CU; a resident grid whose next tile's loads go ahead of the stores
+// spilled).
 // Earlier forms: a fragment's reads waited for right ahead of its products, and the loads of the next
 // block with a tile's scale, 168 us; the barrier ahead of the last group only, 124.  A wave's
 // priority raised for half of the waves: 114 to 117.  128 x 128 tiles on four waves: 146.
@@ -556,7 +558,7 @@ __global__ __launch_bounds__(KS * (BM / WM) * (BN / WN) * 64) void k_f8_split(F8
 // ------------------------------------------------------------------------ tile choice
 
 // The form that is estimated to take the least time for a block of contraction: `one` us for up to 256
-// tiles (one a CU), else `two` for each 512; of the largest form one workgroup fills a CU.  Measured us of whole products with each form, 16-bit
+// tiles (one a CU), else `two` for each 512; of the largest form one workgroup fills a CU.  Measured us of whole products with each form, bf16
 // results, B by tiles:
 //   M x N x K            256 x 256   128 x 128   128 x 64   64 x 64   64 x 64, split
 //   8192 x 8192 x 2048   152         185         257        282
