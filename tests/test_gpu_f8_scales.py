@@ -112,8 +112,11 @@ def test_blocks_that_add_nothing(m, n, k, blocks, out):
     else:
         tb[:, 0] = 2.0**44
     y = bitopt.f8_matmul(a, sa, b, tb, k, b_blocks=blocks, dtype=DT[out])
-    va, vb = decoded(a[:, 128:], sa[1:], k - 128, "e4m3", "rows") if k > 128 else torch.zeros(m, 1, device="cuda").double(), None
-    vb = decoded(b[:, 128:], tb[1:] if blocks == "rows" else tb[:, 1:], k - 128, "e4m3", blocks) if k > 128 else torch.zeros(n, 1, device="cuda").double()
+    if k == 128:
+        assert (y == 0).all()
+        return
+    va = decoded(a[:, 128:], sa[1:], k - 128, "e4m3", "rows")
+    vb = decoded(b[:, 128:], tb[1:] if blocks == "rows" else tb[:, 1:], k - 128, "e4m3", blocks)
     check(y, va, vb, out, m)
 
 
@@ -128,7 +131,7 @@ def test_other_results_keep_their_bits(m, n, k, blocks, out):
     call = lambda a, sa, sb, **kw: bitopt.f8_matmul(a, sa, b, sb, k, "e5m2", b_blocks=blocks, **kw)
     want = call(a, sa, sb, dtype=DT[out])
     ta, ca = sa.clone(), a.clone()
-    zero, small, large = [r for r in (0, m // 2, m - 1)][:max(1, m // 3) and 3]
+    zero, small, large = 0, m // 2, m - 1
     ta[:, small] = spread(sa[:, small], 1, -120, -115)
     ta[:, large] = spread(sa[:, large], 2, 110, 115)
     ca[zero], ta[:, zero] = 0, 2.0**-126
